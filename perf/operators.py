@@ -67,7 +67,9 @@ def draw(rng):
         most = 8192 * 9728 * 2560 // (n * k)
         m = _log_int(rng, 1, max(1, min(8192, most)))
         a, b = rng.choice([(FP8, FP8), (FP8, FP4), (FP4, FP4), (FP4, FP8)])
-        return {"op": op, "m": m, "n": n, "k": k, "a": a, "b": b, "out": rng.choice(["bf16", "bf16", "f32"])}
+        # an E4M3 operand gives a BF16 result; two E2M1 operands an FP32 one too
+        out = rng.choice(["bf16", "f32"]) if a == b == FP4 else "bf16"
+        return {"op": op, "m": m, "n": n, "k": k, "a": a, "b": b, "out": out}
     n = 32 * _log_int(rng, 2, 256)
     m = _log_int(rng, 1, min(65536, 16_000_000 // n))
     if op == "codec":
