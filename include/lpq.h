@@ -41,8 +41,9 @@
  *    uint16_t bit patterns, E4M3 codes as uint8_t (float8_e4m3fn).
  *  - Every argument check that can run on the host runs before anything is
  *    enqueued; on failure nothing is enqueued and the status says why.
- *  - Alignment (LPQ_ERR_ALIGN otherwise): MXFP8 and NVFP4 BF16 arrays 16
- *    bytes, MXFP8 code arrays 8 bytes, NVFP4 packed arrays 4 bytes; the
+ *  - Alignment (LPQ_ERR_ALIGN otherwise): MXFP8, MXFP4 and NVFP4 BF16 arrays
+ *    16 bytes, MXFP8 code arrays 8 bytes, MXFP4 and NVFP4 packed arrays 4
+ *    bytes (other calls state their own); the
  *    block-wise FP8 calls accept any 2-byte aligned BF16 and any code array
  *    (rows that are not 16-byte aligned take a slower path).  FP32 arrays
  *    (scales, amax, global scales) must be 4-byte aligned; byte scale arrays
@@ -67,7 +68,7 @@ typedef enum lpq_status {
 #endif
     LPQ_OK = 0,
     LPQ_ERR_NULL = 1,   /* a required pointer is NULL                                   */
-    LPQ_ERR_SHAPE = 2,  /* M or N <= 0, N not a multiple of the block (32 MXFP8, 16
+    LPQ_ERR_SHAPE = 2,  /* M or N <= 0, N not a multiple of the block (32 MXFP8/4, 16
                            NVFP4), a tensor count <= 0, or a tensor beyond the size
                            limits (M * N above 2^40 for every call; tighter limits are
                            stated where a call has one)                                 */
@@ -128,6 +129,31 @@ lpq_status lpq_dequantize_mxfp8(const uint8_t* q, const uint8_t* e, int64_t M, i
 lpq_status lpq_quantize_mxfp8_floor(const uint16_t* w, int64_t M, int64_t N, uint8_t* q, uint8_t* e, void* stream);
 
 /* ======================================================================== */
+/* MXFP4, of the OCP Microscaling (MX) Formats specification v1.0 -- E2M1
+ * values in 1 x 32 blocks along a row, one UE8M0 (power-of-two) scale byte
+ * per block.  N % 32 == 0.
+ *   amax  = max |w| over the 32 elements of the block
+ *   e     = the smallest integer with amax <= 6 * 2^e, clamped to e >= -127
+ *           (no element saturates); _floor calls: floor(log2 amax) - 2, same
+ *           clamp (the specification's section 6.3: an element between
+ *           6 * 2^e and 8 * 2^e saturates)
+ *   byte  = e + 127                               (never 255)
+ *   code  = E2M1(w * 2^-e)                        (exact scaling, one rounding)
+ *   y     = BF16(E2M1value(code) * 2^e)
+ * w, x, y: [M, N] BF16, 16-byte aligned.  p: [M, N/2] packed codes, element 2j
+ * in the low nibble of byte j, 4-byte aligned.  e: [M, N/32] uint8, any
+ * alignment. */
+lpq_status lpq_quantize_mxfp4(const uint16_t* w, int64_t M, int64_t N, uint8_t* p, uint8_t* e, void* stream);
+lpq_status lpq_quantize_mxfp4_floor(const uint16_t* w, int64_t M, int64_t N, uint8_t* p, uint8_t* e, void* stream);
+lpq_status lpq_dequantize_mxfp4(const uint8_t* p, const uint8_t* e, int64_t M, int64_t N, uint16_t* y, void* stream);
+
+/* Fake quantization (the forward pass of a straight-through estimator): y =
+ * dequantize(quantize(x)) bit for bit, no codes stored.  x and y may not
+ * overlap, except that y may be x itself. */
+lpq_status lpq_mxfp4_qdq(const uint16_t* x, int64_t M, int64_t N, uint16_t* y, void* stream);
+lpq_status lpq_mxfp4_qdq_floor(const uint16_t* x, int64_t M, int64_t N, uint16_t* y, void* stream);
+
+/* ======================================================================== */
 /* NVFP4: "Low Precision RL", "4. NVFP4"; "verl NVFP4 QAT", sections 2.3-2.5
  * and 3.3 -- E2M1 values in 1 x 16 blocks, an E4M3 block scale and an FP32
  * global scale.  N % 16 == 0.
@@ -182,6 +208,9 @@ lpq_status lpq_nvfp4_qdq(const uint16_t* x, int64_t M, int64_t N, const float* a
  *   dequantize_fp8blk_grouped   codes [M,N]    BF16 [M,N]        FP32 tiles (in)
  *   quantize_mxfp8_grouped      BF16           codes             uint8 [M,N/32] (out)
  *   dequantize_mxfp8_grouped    codes          BF16              uint8 (in)
+ *   quantize_mxfp4_grouped      BF16           packed [M,N/2]    uint8 [M,N/32] (out)
+ *   dequantize_mxfp4_grouped    packed         BF16              uint8 (in)
+ *   mxfp4_qdq_grouped           BF16           BF16              unused
  *   nvfp4_amax_grouped          BF16           unused            unused
  *   quantize_nvfp4_grouped      BF16           packed [M,N/2]    E4M3 [M,N/16] (out)
  *   dequantize_nvfp4_grouped    packed         BF16              E4M3 (in)
@@ -210,6 +239,12 @@ lpq_status lpq_quantize_mxfp8_grouped(const lpq_tensor* host, const lpq_tensor* 
                                       void* stream);
 lpq_status lpq_dequantize_mxfp8_grouped(const lpq_tensor* host, const lpq_tensor* dev, int32_t n,
                                         void* stream);
+
+lpq_status lpq_quantize_mxfp4_grouped(const lpq_tensor* host, const lpq_tensor* dev, int32_t n, void* stream);
+lpq_status lpq_quantize_mxfp4_floor_grouped(const lpq_tensor* host, const lpq_tensor* dev, int32_t n, void* stream);
+lpq_status lpq_dequantize_mxfp4_grouped(const lpq_tensor* host, const lpq_tensor* dev, int32_t n, void* stream);
+lpq_status lpq_mxfp4_qdq_grouped(const lpq_tensor* host, const lpq_tensor* dev, int32_t n, void* stream);
+lpq_status lpq_mxfp4_qdq_floor_grouped(const lpq_tensor* host, const lpq_tensor* dev, int32_t n, void* stream);
 
 /* group_amax: n_groups FP32 (device).  accumulate == 0: the group slots are
  * first set to 0, then group_amax[group] = max over the group's members of

@@ -71,6 +71,16 @@ _SIG = {
     "lpq_dequantize_mxfp8": (_int, [_vp, _vp, _i64, _i64, _vp, _vp]),
     "lpq_quantize_mxfp8_floor": (_int, [_vp, _i64, _i64, _vp, _vp, _vp]),
     "lpq_quantize_mxfp8_floor_grouped": (_int, [_tp, _vp, _i32, _vp]),
+    "lpq_quantize_mxfp4": (_int, [_vp, _i64, _i64, _vp, _vp, _vp]),
+    "lpq_quantize_mxfp4_floor": (_int, [_vp, _i64, _i64, _vp, _vp, _vp]),
+    "lpq_dequantize_mxfp4": (_int, [_vp, _vp, _i64, _i64, _vp, _vp]),
+    "lpq_mxfp4_qdq": (_int, [_vp, _i64, _i64, _vp, _vp]),
+    "lpq_mxfp4_qdq_floor": (_int, [_vp, _i64, _i64, _vp, _vp]),
+    "lpq_quantize_mxfp4_grouped": (_int, [_tp, _vp, _i32, _vp]),
+    "lpq_quantize_mxfp4_floor_grouped": (_int, [_tp, _vp, _i32, _vp]),
+    "lpq_dequantize_mxfp4_grouped": (_int, [_tp, _vp, _i32, _vp]),
+    "lpq_mxfp4_qdq_grouped": (_int, [_tp, _vp, _i32, _vp]),
+    "lpq_mxfp4_qdq_floor_grouped": (_int, [_tp, _vp, _i32, _vp]),
     "lpq_nvfp4_global_scale_reciprocal": (_int, [_vp, _i32, _vp, _vp]),
     "lpq_nvfp4_global_scale": (_int, [_vp, _i32, _vp, _vp]),
     "lpq_quantize_nvfp4_ex": (_int, [_vp, _i64, _i64, _vp, _int, _vp, _vp, _vp, _vp]),
@@ -254,6 +264,56 @@ def lpq_dequantize_mxfp8(q, e, y=None, stream=None):
     _check(_L.lpq_dequantize_mxfp8(q.data_ptr(), e.data_ptr(), M, N, y.data_ptr(), _stream(stream)),
            "lpq_dequantize_mxfp8")
     return y
+
+
+# --------------------------------------------------------------------------- MXFP4
+
+def _mxfp4_quantize(fn, where, w, p, e, stream):
+    w = _bf16_in(w, "w")
+    M, N = w.shape
+    p, e = _outs(w, (p, "p", M * (N // 2), (M, max(N // 2, 1)), torch.uint8, 1),
+                 (e, "e", M * (N // 32), (M, max(N // 32, 1)), torch.uint8, 1))
+    _check(fn(w.data_ptr(), M, N, p.data_ptr(), e.data_ptr(), _stream(stream)), where)
+    return p, e
+
+
+def lpq_quantize_mxfp4(w, p=None, e=None, stream=None):
+    """BF16 [M,N] (N % 32 == 0) -> (packed E2M1 codes [M,N/2] uint8, UE8M0 bytes [M,N/32] uint8)."""
+    return _mxfp4_quantize(_L.lpq_quantize_mxfp4, "lpq_quantize_mxfp4", w, p, e, stream)
+
+
+def lpq_quantize_mxfp4_floor(w, p=None, e=None, stream=None):
+    """As lpq_quantize_mxfp4, with the OCP MX floor exponent rule (saturating)."""
+    return _mxfp4_quantize(_L.lpq_quantize_mxfp4_floor, "lpq_quantize_mxfp4_floor", w, p, e, stream)
+
+
+def lpq_dequantize_mxfp4(p, e, y=None, stream=None):
+    """(packed [M,N/2], UE8M0 bytes [M,N/32]) -> BF16 [M,N]."""
+    p = _codes_in(p, "p")
+    M, N = p.shape[0], p.shape[1] * 2
+    _arg(e, "e", p, M * (N // 32), esize=1)
+    y = _out(y, "y", p, 2 * M * N, (M, N), torch.bfloat16, 2)
+    _check(_L.lpq_dequantize_mxfp4(p.data_ptr(), e.data_ptr(), M, N, y.data_ptr(), _stream(stream)),
+           "lpq_dequantize_mxfp4")
+    return y
+
+
+def _mxfp4_qdq(fn, where, x, y, stream):
+    x = _bf16_in(x, "x")
+    M, N = x.shape
+    y = _out(y, "y", x, 2 * M * N, (M, N), torch.bfloat16, 2)
+    _check(fn(x.data_ptr(), M, N, y.data_ptr(), _stream(stream)), where)
+    return y
+
+
+def lpq_mxfp4_qdq(x, y=None, stream=None):
+    """MXFP4 fake quantization of BF16 [M,N] (a straight-through estimator's forward pass)."""
+    return _mxfp4_qdq(_L.lpq_mxfp4_qdq, "lpq_mxfp4_qdq", x, y, stream)
+
+
+def lpq_mxfp4_qdq_floor(x, y=None, stream=None):
+    """As lpq_mxfp4_qdq, with the OCP MX floor exponent rule (saturating)."""
+    return _mxfp4_qdq(_L.lpq_mxfp4_qdq_floor, "lpq_mxfp4_qdq_floor", x, y, stream)
 
 
 # --------------------------------------------------------------------------- NVFP4
@@ -506,6 +566,9 @@ _GROUPED_BYTES = {
     "fp8blk_dq": lambda MN, t, G: (MN, 2 * MN, t),
     "mxfp8_q": lambda MN, t, G: (2 * MN, MN, MN // 32),
     "mxfp8_dq": lambda MN, t, G: (MN, 2 * MN, MN // 32),
+    "mxfp4_q": lambda MN, t, G: (2 * MN, MN // 2, MN // 32),
+    "mxfp4_dq": lambda MN, t, G: (MN // 2, 2 * MN, MN // 32),
+    "mxfp4_qdq": lambda MN, t, G: (2 * MN, 2 * MN, None),
     "nvfp4_amax": lambda MN, t, G: (2 * MN, None, None),
     "nvfp4_q": lambda MN, t, G: (2 * MN, MN // 2, MN // 16),
     "nvfp4_dq": lambda MN, t, G: (MN // 2, 2 * MN, MN // 16),
@@ -626,6 +689,30 @@ def lpq_quantize_mxfp8_floor_grouped(table: TensorTable, stream=None):
 def lpq_dequantize_mxfp8_grouped(table: TensorTable, stream=None):
     _check(_L.lpq_dequantize_mxfp8_grouped(*table.check("mxfp8_dq").args(), _stream(stream)),
            "lpq_dequantize_mxfp8_grouped")
+
+
+def lpq_quantize_mxfp4_grouped(table: TensorTable, stream=None):
+    _check(_L.lpq_quantize_mxfp4_grouped(*table.check("mxfp4_q").args(), _stream(stream)),
+           "lpq_quantize_mxfp4_grouped")
+
+
+def lpq_quantize_mxfp4_floor_grouped(table: TensorTable, stream=None):
+    _check(_L.lpq_quantize_mxfp4_floor_grouped(*table.check("mxfp4_q").args(), _stream(stream)),
+           "lpq_quantize_mxfp4_floor_grouped")
+
+
+def lpq_dequantize_mxfp4_grouped(table: TensorTable, stream=None):
+    _check(_L.lpq_dequantize_mxfp4_grouped(*table.check("mxfp4_dq").args(), _stream(stream)),
+           "lpq_dequantize_mxfp4_grouped")
+
+
+def lpq_mxfp4_qdq_grouped(table: TensorTable, stream=None):
+    _check(_L.lpq_mxfp4_qdq_grouped(*table.check("mxfp4_qdq").args(), _stream(stream)), "lpq_mxfp4_qdq_grouped")
+
+
+def lpq_mxfp4_qdq_floor_grouped(table: TensorTable, stream=None):
+    _check(_L.lpq_mxfp4_qdq_floor_grouped(*table.check("mxfp4_qdq").args(), _stream(stream)),
+           "lpq_mxfp4_qdq_floor_grouped")
 
 
 def lpq_nvfp4_amax_grouped(table: TensorTable, group_amax, accumulate=False, stream=None):

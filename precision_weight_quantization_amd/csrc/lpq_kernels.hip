@@ -46,6 +46,7 @@ using namespace lpq;
 
 #include "lpq_flat.hpp"
 #include "lpq_mxfp8.hpp"
+#include "lpq_mxfp4.hpp"
 #include "lpq_nvfp4.hpp"
 #include "lpq_int4.hpp"
 #include "lpq_fp8blk.hpp"
@@ -72,7 +73,8 @@ inline lpq_status launched() {
 }
 
 enum Kind {
-    FP8BLK_Q, FP8BLK_QW, FP8BLK_DQ, FP8BLK_DQF, MXFP8_Q, MXFP8_QF, MXFP8_DQ, NV_AMAX, NV_Q, NV_DQ, NV_QDQ, NV_QDQ_W,
+    FP8BLK_Q, FP8BLK_QW, FP8BLK_DQ, FP8BLK_DQF, MXFP8_Q, MXFP8_QF, MXFP8_DQ,
+    MXFP4_Q, MXFP4_QF, MXFP4_DQ, MXFP4_QDQ, MXFP4_QDQF, NV_AMAX, NV_Q, NV_DQ, NV_QDQ, NV_QDQ_W,
     I4_Q32, I4_Q128, I4_DQ32, I4_DQ128, I4_QDQ32, I4_QDQ128,
     RQ_FP8, RQ_MX, RQ_AMAX, RQ_NV
 };
@@ -88,7 +90,8 @@ lpq_status check_tensor(Kind k, const lpq_tensor& t, int32_t n_groups) {
     if (t.rows > (int64_t(1) << 40) / t.cols) return LPQ_ERR_SHAPE;   // element count overflow guard
     if (!t.src) return LPQ_ERR_NULL;
     if (k != NV_AMAX && !t.dst) return LPQ_ERR_NULL;
-    if (k != NV_AMAX && k != NV_QDQ && k != I4_QDQ32 && k != I4_QDQ128 && !t.scale) return LPQ_ERR_NULL;
+    if (k != NV_AMAX && k != NV_QDQ && k != I4_QDQ32 && k != I4_QDQ128 && k != MXFP4_QDQ && k != MXFP4_QDQF && !t.scale)
+        return LPQ_ERR_NULL;
     if (t.reserved != 0) return LPQ_ERR_ARG;
     switch (k) {
     case FP8BLK_Q:
@@ -108,6 +111,20 @@ lpq_status check_tensor(Kind k, const lpq_tensor& t, int32_t n_groups) {
     case MXFP8_DQ:
         if (t.cols % 32) return LPQ_ERR_SHAPE;
         if (!aligned(t.src, 8) || !aligned(t.dst, 16)) return LPQ_ERR_ALIGN;
+        break;
+    case MXFP4_Q:
+    case MXFP4_QF:
+        if (t.cols % 32) return LPQ_ERR_SHAPE;
+        if (!aligned(t.src, 16) || !aligned(t.dst, 4)) return LPQ_ERR_ALIGN;
+        break;
+    case MXFP4_DQ:
+        if (t.cols % 32) return LPQ_ERR_SHAPE;
+        if (!aligned(t.src, 4) || !aligned(t.dst, 16)) return LPQ_ERR_ALIGN;
+        break;
+    case MXFP4_QDQ:
+    case MXFP4_QDQF:
+        if (t.cols % 32) return LPQ_ERR_SHAPE;
+        if (!aligned(t.src, 16) || !aligned(t.dst, 16)) return LPQ_ERR_ALIGN;
         break;
     case NV_AMAX:
     case NV_Q:
@@ -167,6 +184,11 @@ int64_t units(Kind k, const lpq_tensor& t) {
     case MXFP8_Q:
     case MXFP8_QF: return (n + chunk_elems<LPQ_MXQ_U, LPQ_MXQ_T>() - 1) / chunk_elems<LPQ_MXQ_U, LPQ_MXQ_T>();
     case MXFP8_DQ: return (n + chunk_elems<LPQ_MXD_U, LPQ_MXD_T>() - 1) / chunk_elems<LPQ_MXD_U, LPQ_MXD_T>();
+    case MXFP4_Q:
+    case MXFP4_QF: return (n + chunk_elems<LPQ_MX4Q_U, LPQ_MX4Q_T>() - 1) / chunk_elems<LPQ_MX4Q_U, LPQ_MX4Q_T>();
+    case MXFP4_DQ: return (n + chunk_elems<LPQ_MX4D_U, LPQ_MX4D_T>() - 1) / chunk_elems<LPQ_MX4D_U, LPQ_MX4D_T>();
+    case MXFP4_QDQ:
+    case MXFP4_QDQF: return (n + chunk_elems<LPQ_MX4QDQ_U, LPQ_MX4QDQ_T>() - 1) / chunk_elems<LPQ_MX4QDQ_U, LPQ_MX4QDQ_T>();
     case NV_AMAX: return (n + chunk_elems<LPQ_AMAX_U, LPQ_AMAX_T>() - 1) / chunk_elems<LPQ_AMAX_U, LPQ_AMAX_T>();
     case NV_Q: return (n + chunk_elems<LPQ_NVQ_U, LPQ_NVQ_T>() - 1) / chunk_elems<LPQ_NVQ_U, LPQ_NVQ_T>();
     case NV_DQ: return (n + chunk_elems<LPQ_NVD_U, LPQ_NVD_T>() - 1) / chunk_elems<LPQ_NVD_U, LPQ_NVD_T>();
@@ -209,6 +231,11 @@ void dispatch(Kind k, dim3 grid, hipStream_t stream, const lpq_tensor* tab, cons
         case MXFP8_Q: hipLaunchKernelGGL((k_mxfp8_quant<LPQ_MXQ_U, LPQ_MXQ_T, true>), grid, dim3(LPQ_MXQ_T), 0, stream, tab, one, map); break;
         case MXFP8_QF: hipLaunchKernelGGL((k_mxfp8_quant<LPQ_MXQ_U, LPQ_MXQ_T, true, true>), grid, dim3(LPQ_MXQ_T), 0, stream, tab, one, map); break;
         case MXFP8_DQ: hipLaunchKernelGGL((k_mxfp8_dequant<LPQ_MXD_U, LPQ_MXD_T, true>), grid, dim3(LPQ_MXD_T), 0, stream, tab, one, map); break;
+        case MXFP4_Q: hipLaunchKernelGGL((k_mxfp4_quant<LPQ_MX4Q_U, LPQ_MX4Q_T, true>), grid, dim3(LPQ_MX4Q_T), 0, stream, tab, one, map); break;
+        case MXFP4_QF: hipLaunchKernelGGL((k_mxfp4_quant<LPQ_MX4Q_U, LPQ_MX4Q_T, true, true>), grid, dim3(LPQ_MX4Q_T), 0, stream, tab, one, map); break;
+        case MXFP4_DQ: hipLaunchKernelGGL((k_mxfp4_dequant<LPQ_MX4D_U, LPQ_MX4D_T, true>), grid, dim3(LPQ_MX4D_T), 0, stream, tab, one, map); break;
+        case MXFP4_QDQ: hipLaunchKernelGGL((k_mxfp4_qdq<LPQ_MX4QDQ_U, LPQ_MX4QDQ_T, true>), grid, dim3(LPQ_MX4QDQ_T), 0, stream, tab, one, map); break;
+        case MXFP4_QDQF: hipLaunchKernelGGL((k_mxfp4_qdq<LPQ_MX4QDQ_U, LPQ_MX4QDQ_T, true, true>), grid, dim3(LPQ_MX4QDQ_T), 0, stream, tab, one, map); break;
         case NV_AMAX: hipLaunchKernelGGL((k_amax<LPQ_AMAX_U, LPQ_AMAX_T, true>), grid, dim3(LPQ_AMAX_T), 0, stream, tab, one, map, fb); break;
         case NV_Q: hipLaunchKernelGGL((k_nvfp4_quant<LPQ_NVQ_U, LPQ_NVQ_T, true>), grid, dim3(LPQ_NVQ_T), 0, stream, tab, one, map, fa, fb); break;
         case NV_DQ: hipLaunchKernelGGL((k_nvfp4_dequant<LPQ_NVD_U, LPQ_NVD_T, true>), grid, dim3(LPQ_NVD_T), 0, stream, tab, one, map, fa); break;
@@ -232,6 +259,11 @@ void dispatch(Kind k, dim3 grid, hipStream_t stream, const lpq_tensor* tab, cons
         case MXFP8_Q: hipLaunchKernelGGL((k_mxfp8_quant<LPQ_MXQ_U, LPQ_MXQ_T, false>), grid, dim3(LPQ_MXQ_T), 0, stream, tab, one, map); break;
         case MXFP8_QF: hipLaunchKernelGGL((k_mxfp8_quant<LPQ_MXQ_U, LPQ_MXQ_T, false, true>), grid, dim3(LPQ_MXQ_T), 0, stream, tab, one, map); break;
         case MXFP8_DQ: hipLaunchKernelGGL((k_mxfp8_dequant<LPQ_MXD_U, LPQ_MXD_T, false>), grid, dim3(LPQ_MXD_T), 0, stream, tab, one, map); break;
+        case MXFP4_Q: hipLaunchKernelGGL((k_mxfp4_quant<LPQ_MX4Q_U, LPQ_MX4Q_T, false>), grid, dim3(LPQ_MX4Q_T), 0, stream, tab, one, map); break;
+        case MXFP4_QF: hipLaunchKernelGGL((k_mxfp4_quant<LPQ_MX4Q_U, LPQ_MX4Q_T, false, true>), grid, dim3(LPQ_MX4Q_T), 0, stream, tab, one, map); break;
+        case MXFP4_DQ: hipLaunchKernelGGL((k_mxfp4_dequant<LPQ_MX4D_U, LPQ_MX4D_T, false>), grid, dim3(LPQ_MX4D_T), 0, stream, tab, one, map); break;
+        case MXFP4_QDQ: hipLaunchKernelGGL((k_mxfp4_qdq<LPQ_MX4QDQ_U, LPQ_MX4QDQ_T, false>), grid, dim3(LPQ_MX4QDQ_T), 0, stream, tab, one, map); break;
+        case MXFP4_QDQF: hipLaunchKernelGGL((k_mxfp4_qdq<LPQ_MX4QDQ_U, LPQ_MX4QDQ_T, false, true>), grid, dim3(LPQ_MX4QDQ_T), 0, stream, tab, one, map); break;
         case NV_AMAX: hipLaunchKernelGGL((k_amax<LPQ_AMAX_U, LPQ_AMAX_T, false>), grid, dim3(LPQ_AMAX_T), 0, stream, tab, one, map, fb); break;
         case NV_Q: hipLaunchKernelGGL((k_nvfp4_quant<LPQ_NVQ_U, LPQ_NVQ_T, false>), grid, dim3(LPQ_NVQ_T), 0, stream, tab, one, map, fa, fb); break;
         case NV_DQ: hipLaunchKernelGGL((k_nvfp4_dequant<LPQ_NVD_U, LPQ_NVD_T, false>), grid, dim3(LPQ_NVD_T), 0, stream, tab, one, map, fa); break;
@@ -610,6 +642,46 @@ lpq_status lpq_quantize_mxfp8_floor(const uint16_t* w, int64_t M, int64_t N, uin
 
 lpq_status lpq_quantize_mxfp8_floor_grouped(const lpq_tensor* host, const lpq_tensor* dev, int32_t n, void* stream) {
     return grouped(MXFP8_QF, host, dev, n, 0, nullptr, nullptr, stream);
+}
+
+lpq_status lpq_quantize_mxfp4(const uint16_t* w, int64_t M, int64_t N, uint8_t* p, uint8_t* e, void* stream) {
+    return single(MXFP4_Q, make_one(w, p, e, M, N), nullptr, nullptr, stream);
+}
+
+lpq_status lpq_quantize_mxfp4_floor(const uint16_t* w, int64_t M, int64_t N, uint8_t* p, uint8_t* e, void* stream) {
+    return single(MXFP4_QF, make_one(w, p, e, M, N), nullptr, nullptr, stream);
+}
+
+lpq_status lpq_dequantize_mxfp4(const uint8_t* p, const uint8_t* e, int64_t M, int64_t N, uint16_t* y, void* stream) {
+    return single(MXFP4_DQ, make_one(p, y, const_cast<uint8_t*>(e), M, N), nullptr, nullptr, stream);
+}
+
+lpq_status lpq_mxfp4_qdq(const uint16_t* x, int64_t M, int64_t N, uint16_t* y, void* stream) {
+    return single(MXFP4_QDQ, make_one(x, y, nullptr, M, N), nullptr, nullptr, stream);
+}
+
+lpq_status lpq_mxfp4_qdq_floor(const uint16_t* x, int64_t M, int64_t N, uint16_t* y, void* stream) {
+    return single(MXFP4_QDQF, make_one(x, y, nullptr, M, N), nullptr, nullptr, stream);
+}
+
+lpq_status lpq_quantize_mxfp4_grouped(const lpq_tensor* host, const lpq_tensor* dev, int32_t n, void* stream) {
+    return grouped(MXFP4_Q, host, dev, n, 0, nullptr, nullptr, stream);
+}
+
+lpq_status lpq_quantize_mxfp4_floor_grouped(const lpq_tensor* host, const lpq_tensor* dev, int32_t n, void* stream) {
+    return grouped(MXFP4_QF, host, dev, n, 0, nullptr, nullptr, stream);
+}
+
+lpq_status lpq_dequantize_mxfp4_grouped(const lpq_tensor* host, const lpq_tensor* dev, int32_t n, void* stream) {
+    return grouped(MXFP4_DQ, host, dev, n, 0, nullptr, nullptr, stream);
+}
+
+lpq_status lpq_mxfp4_qdq_grouped(const lpq_tensor* host, const lpq_tensor* dev, int32_t n, void* stream) {
+    return grouped(MXFP4_QDQ, host, dev, n, 0, nullptr, nullptr, stream);
+}
+
+lpq_status lpq_mxfp4_qdq_floor_grouped(const lpq_tensor* host, const lpq_tensor* dev, int32_t n, void* stream) {
+    return grouped(MXFP4_QDQF, host, dev, n, 0, nullptr, nullptr, stream);
 }
 
 lpq_status lpq_nvfp4_global_scale_reciprocal(const float* group_amax, int32_t n_groups, float* out, void* stream) {

@@ -167,3 +167,31 @@
 #ifndef LPQ_RQN_T
 #define LPQ_RQN_T LPQ_FLAT_THREADS
 #endif
+// MXFP4 codec (vectors per lane, workgroup size, load order).
+#ifndef LPQ_MX4Q_U
+#define LPQ_MX4Q_U 2
+#endif
+#ifndef LPQ_MX4Q_T
+#define LPQ_MX4Q_T 128
+#endif
+#ifndef LPQ_MX4Q_AHEAD
+#define LPQ_MX4Q_AHEAD 1
+#endif
+#ifndef LPQ_MX4D_U
+#define LPQ_MX4D_U 2
+#endif
+#ifndef LPQ_MX4D_T
+#define LPQ_MX4D_T 512
+#endif
+#ifndef LPQ_MX4D_AHEAD
+#define LPQ_MX4D_AHEAD 0
+#endif
+#ifndef LPQ_MX4QDQ_U
+#define LPQ_MX4QDQ_U 2
+#endif
+#ifndef LPQ_MX4QDQ_T
+#define LPQ_MX4QDQ_T 128
+#endif
+#ifndef LPQ_MX4QDQ_AHEAD
+#define LPQ_MX4QDQ_AHEAD 1
+#endif
