@@ -154,6 +154,25 @@ lpq_status lpq_mxfp4_qdq(const uint16_t* x, int64_t M, int64_t N, uint16_t* y, v
 lpq_status lpq_mxfp4_qdq_floor(const uint16_t* x, int64_t M, int64_t N, uint16_t* y, void* stream);
 
 /* ======================================================================== */
+/* Two-way microscaled quantization, one read of w: the codes of w with blocks
+ * along its columns' direction, transposed, and on request the row form of
+ * lpq_quantize_mxfp8 / lpq_quantize_mxfp4 too.  A microscaled product contracts
+ * along the blocks, so the two products of a backward pass (of the output's
+ * gradient with the weight, and with the input) need these forms.
+ *   w       [M, N] BF16, N % 32 == 0, any M; 16-byte aligned
+ *   q, e    the row form, bit for bit what lpq_quantize_mxfp8[_floor] or
+ *           lpq_quantize_mxfp4[_floor] writes, aligned alike; both NULL: not wanted
+ *   qt, et  the column form: the row form of the transpose of w with zero rows
+ *           appended up to Mp = M rounded up to 32.  qt: [N, Mp] codes, or pt:
+ *           [N, Mp/2] packed; 16-byte aligned.  et: [N, Mp/32] bytes.
+ * floor_rule: 0 the default exponent rule, 1 the floor rule.  Another
+ * floor_rule, and outputs that overlap w or one another: LPQ_ERR_ARG. */
+lpq_status lpq_quantize_mxfp8_transposed(const uint16_t* w, int64_t M, int64_t N, int floor_rule, uint8_t* q, uint8_t* e,
+                                         uint8_t* qt, uint8_t* et, void* stream);
+lpq_status lpq_quantize_mxfp4_transposed(const uint16_t* w, int64_t M, int64_t N, int floor_rule, uint8_t* p, uint8_t* e,
+                                         uint8_t* pt, uint8_t* et, void* stream);
+
+/* ======================================================================== */
 /* NVFP4: "Low Precision RL", "4. NVFP4"; "verl NVFP4 QAT", sections 2.3-2.5
  * and 3.3 -- E2M1 values in 1 x 16 blocks, an E4M3 block scale and an FP32
  * global scale.  N % 16 == 0.

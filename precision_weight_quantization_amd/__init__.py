@@ -81,6 +81,8 @@ _SIG = {
     "lpq_dequantize_mxfp4_grouped": (_int, [_tp, _vp, _i32, _vp]),
     "lpq_mxfp4_qdq_grouped": (_int, [_tp, _vp, _i32, _vp]),
     "lpq_mxfp4_qdq_floor_grouped": (_int, [_tp, _vp, _i32, _vp]),
+    "lpq_quantize_mxfp8_transposed": (_int, [_vp, _i64, _i64, _int, _vp, _vp, _vp, _vp, _vp]),
+    "lpq_quantize_mxfp4_transposed": (_int, [_vp, _i64, _i64, _int, _vp, _vp, _vp, _vp, _vp]),
     "lpq_nvfp4_global_scale_reciprocal": (_int, [_vp, _i32, _vp, _vp]),
     "lpq_nvfp4_global_scale": (_int, [_vp, _i32, _vp, _vp]),
     "lpq_quantize_nvfp4_ex": (_int, [_vp, _i64, _i64, _vp, _int, _vp, _vp, _vp, _vp]),
@@ -134,6 +136,17 @@ def _stream(stream) -> int:
     if stream is None:
         stream = torch.cuda.current_stream()
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _launch(fn, where: str, like, stream, *args) -> None:
+    """Call ``fn(*args, stream)`` with the device of ``like`` current, on the given
+    stream or that device's current one."""
+    index = like.device.index
+    if index == torch.cuda.current_device():
+        _check(fn(*args, _stream(stream)), where)
+    else:
+        with torch.cuda.device(index):
+            _check(fn(*args, _stream(stream)), where)
 
 
 def _ptr(t) -> int:
@@ -314,6 +327,39 @@ def lpq_mxfp4_qdq(x, y=None, stream=None):
 def lpq_mxfp4_qdq_floor(x, y=None, stream=None):
     """As lpq_mxfp4_qdq, with the OCP MX floor exponent rule (saturating)."""
     return _mxfp4_qdq(_L.lpq_mxfp4_qdq_floor, "lpq_mxfp4_qdq_floor", x, y, stream)
+
+
+# --------------------------------------------------------------------------- two-way MXFP8 / MXFP4
+
+def _mx_transposed(fn, where, per_byte, dtype, w, rows, floor, qt, et, q, e, stream):
+    w = _bf16_in(w, "w")
+    M, N = w.shape
+    Mp = (M + 31) // 32 * 32
+    if not rows and (q is not None or e is not None):
+        raise ValueError("q and e are outputs of the row form: pass rows=True with them")
+    specs = [(qt, "qt", N * Mp // per_byte, (N, Mp // per_byte), dtype, 1),
+             (et, "et", N * Mp // 32, (N, Mp // 32), torch.uint8, 1)]
+    if rows:
+        specs += [(q, "q", M * (N // per_byte), (M, max(N // per_byte, 1)), dtype, 1),
+                  (e, "e", M * (N // 32), (M, max(N // 32, 1)), torch.uint8, 1)]
+    qt, et, q, e = (_outs(w, *specs) + [None, None])[:4]
+    _launch(fn, where, w, stream, w.data_ptr(), M, N, int(bool(floor)), _ptr(q), _ptr(e), qt.data_ptr(), et.data_ptr())
+    return qt, et, q, e
+
+
+def lpq_quantize_mxfp8_transposed(w, rows=False, floor=False, qt=None, et=None, q=None, e=None, stream=None):
+    """BF16 [M,N] (N % 32 == 0, any M) -> (qt [N,Mp] float8_e4m3fn, et [N,Mp/32] uint8, q, e): the
+    MXFP8 form of the transpose, zero-padded to Mp = M rounded up to 32, and with ``rows`` the row
+    form of lpq_quantize_mxfp8 from the same read (else None, None).  floor: the OCP MX floor
+    exponent rule."""
+    return _mx_transposed(_L.lpq_quantize_mxfp8_transposed, "lpq_quantize_mxfp8_transposed", 1, torch.float8_e4m3fn,
+                          w, rows, floor, qt, et, q, e, stream)
+
+
+def lpq_quantize_mxfp4_transposed(w, rows=False, floor=False, qt=None, et=None, q=None, e=None, stream=None):
+    """As lpq_quantize_mxfp8_transposed in MXFP4: packed codes qt [N,Mp/2] and q [M,N/2] uint8."""
+    return _mx_transposed(_L.lpq_quantize_mxfp4_transposed, "lpq_quantize_mxfp4_transposed", 2, torch.uint8,
+                          w, rows, floor, qt, et, q, e, stream)
 
 
 # --------------------------------------------------------------------------- NVFP4

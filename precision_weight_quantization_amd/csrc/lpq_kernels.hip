@@ -51,6 +51,7 @@ using namespace lpq;
 #include "lpq_int4.hpp"
 #include "lpq_fp8blk.hpp"
 #include "lpq_requant.hpp"
+#include "lpq_mx_transpose.hpp"
 
 
 // ===========================================================================
@@ -537,6 +538,51 @@ lpq_status nvfp4_grouped(Kind k, const lpq_tensor* host, const lpq_tensor* dev, 
     return launch<lpq_tensor>(k, host, dev, n, lpq_tensor{}, group_amax, k == NV_Q ? group_g : nullptr, s, gdiv);
 }
 
+// Two byte ranges that share a byte (either may be empty).
+inline bool overlap(const void* a, int64_t na, const void* b, int64_t nb) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return na > 0 && nb > 0 && x < y + (uintptr_t)nb && y < x + (uintptr_t)na;
+}
+
+template <bool FP4>
+lpq_status mx_transpose(const uint16_t* w, int64_t M, int64_t N, int floor_rule, uint8_t* q, uint8_t* e, uint8_t* qt,
+                        uint8_t* et, void* stream) {
+    if (M <= 0 || N <= 0 || N % 32 || M > (int64_t(1) << 40) / N) return LPQ_ERR_SHAPE;
+    if (!w || !qt || !et || !q != !e) return LPQ_ERR_NULL;
+    if (floor_rule != 0 && floor_rule != 1) return LPQ_ERR_ARG;
+    if (!aligned(w, 16) || !aligned(qt, 16) || (q && !aligned(q, FP4 ? 4 : 8))) return LPQ_ERR_ALIGN;
+    TransposeArgs A;
+    A.w = w;
+    A.q = q;
+    A.e = e;
+    A.qt = qt;
+    A.et = et;
+    A.M = M;
+    A.N = N;
+    A.Mp = (M + 31) / 32 * 32;
+    A.tiles_n = (N + kTrN - 1) / kTrN;
+    const int64_t code = FP4 ? 2 : 1;   // codes in a byte
+    const struct { const void* p; int64_t n; } out[] = {
+        {qt, N * A.Mp / code}, {et, N * A.Mp / 32}, {q, q ? M * N / code : 0}, {e, e ? M * N / 32 : 0}};
+    for (int i = 0; i < 4; i++) {
+        if (overlap(w, 2 * M * N, out[i].p, out[i].n)) return LPQ_ERR_ARG;
+        for (int j = 0; j < i; j++)
+            if (overlap(out[i].p, out[i].n, out[j].p, out[j].n)) return LPQ_ERR_ARG;
+    }
+    const int64_t tiles = (M + kTrM - 1) / kTrM * A.tiles_n;
+    if (tiles > kMaxGridX) return LPQ_ERR_SHAPE;
+    const dim3 grid((unsigned)tiles), block(kTrThreads);
+    const hipStream_t s = (hipStream_t)stream;
+    if (floor_rule) {
+        if (q) hipLaunchKernelGGL((k_mx_transpose<FP4, true, true>), grid, block, 0, s, A);
+        else hipLaunchKernelGGL((k_mx_transpose<FP4, true, false>), grid, block, 0, s, A);
+    } else {
+        if (q) hipLaunchKernelGGL((k_mx_transpose<FP4, false, true>), grid, block, 0, s, A);
+        else hipLaunchKernelGGL((k_mx_transpose<FP4, false, false>), grid, block, 0, s, A);
+    }
+    return launched();
+}
+
 // Host-side checks of an observer call; the workgroup count on success.
 lpq_status observe_args(const uint16_t* x, int64_t M, int64_t N, int observer, const float* state, const float* amax,
                         lpq_tensor* one, int64_t* units) {
@@ -682,6 +728,16 @@ lpq_status lpq_mxfp4_qdq_grouped(const lpq_tensor* host, const lpq_tensor* dev, 
 
 lpq_status lpq_mxfp4_qdq_floor_grouped(const lpq_tensor* host, const lpq_tensor* dev, int32_t n, void* stream) {
     return grouped(MXFP4_QDQF, host, dev, n, 0, nullptr, nullptr, stream);
+}
+
+lpq_status lpq_quantize_mxfp8_transposed(const uint16_t* w, int64_t M, int64_t N, int floor_rule, uint8_t* q, uint8_t* e,
+                                         uint8_t* qt, uint8_t* et, void* stream) {
+    return mx_transpose<false>(w, M, N, floor_rule, q, e, qt, et, stream);
+}
+
+lpq_status lpq_quantize_mxfp4_transposed(const uint16_t* w, int64_t M, int64_t N, int floor_rule, uint8_t* p, uint8_t* e,
+                                         uint8_t* pt, uint8_t* et, void* stream) {
+    return mx_transpose<true>(w, M, N, floor_rule, p, e, pt, et, stream);
 }
 
 lpq_status lpq_nvfp4_global_scale_reciprocal(const float* group_amax, int32_t n_groups, float* out, void* stream) {
