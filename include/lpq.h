@@ -485,6 +485,42 @@ lpq_status lpq_dequantize_int4_grouped(const lpq_tensor* host, const lpq_tensor*
 lpq_status lpq_int4_qdq_grouped(const lpq_tensor* host, const lpq_tensor* dev, int32_t n, int32_t group,
                                 void* stream);
 
+/* ======================================================================== */
+/* Root-mean-square norm with the residual's addition, and its backward pass:
+ * the step in front of a quantized layer.  Per row of N elements:
+ *   h    = BF16(x + residual)    (the stream that the next block adds to;
+ *                                 residual NULL: h is x, and the h output too is NULL)
+ *   rstd = 1 / sqrt(sum(h^2) / N + eps)                    FP32, FP32 sum
+ *   y    = BF16(fl(fl(h * rstd) * gamma))
+ *   q, e = MXFP8 of y, bit for bit what lpq_quantize_mxfp8 makes of it
+ * x, residual, h, y: [M, N] BF16; gamma: [N] BF16 (all 16-byte aligned); rstd:
+ * [M] FP32, NULL if not wanted; q: [M, N] codes, 8-byte aligned; e: [M, N/32].
+ * N % 32 == 0 and N <= 32768 (LPQ_ERR_SHAPE); eps positive and finite
+ * (LPQ_ERR_ARG).  y of lpq_rmsnorm_mxfp8 may be NULL.  h may be x or residual
+ * itself (updated in place); any other overlap of an output: LPQ_ERR_ARG.
+ * The sum of squares is taken in FP32: |h| up to about 1e17. */
+lpq_status lpq_rmsnorm(const uint16_t* x, const uint16_t* residual, const uint16_t* gamma, float eps, int64_t M, int64_t N,
+                       uint16_t* h, float* rstd, uint16_t* y, void* stream);
+lpq_status lpq_rmsnorm_mxfp8(const uint16_t* x, const uint16_t* residual, const uint16_t* gamma, float eps, int64_t M, int64_t N,
+                             uint16_t* h, float* rstd, uint16_t* y, uint8_t* q, uint8_t* e, void* stream);
+
+/* The gradients, from dy (of y, or of the quantized y under a straight-through
+ * estimator) and the forward pass's h and rstd, with n = h * rstd:
+ *   dx     = BF16(rstd * (dy * gamma - n * sum(dy * gamma * n) / N) + dres)
+ *            the gradient of x and, the same, of residual; dres [M, N] BF16:
+ *            the gradient that reaches h along the residual stream, or NULL
+ *   dgamma = sum over the rows of dy * n      [N] FP32, or NULL: not wanted;
+ *            added to what dgamma holds when accumulate != 0
+ * dx may be dy or dres itself; any other overlap of an output: LPQ_ERR_ARG.
+ * workspace: lpq_rmsnorm_backward_workspace(M, N) bytes of device memory (less:
+ * LPQ_ERR_ARG), 16-byte aligned, for this call alone while it runs; NULL and 0
+ * without dgamma.  Sums are FP32 in a fixed order: a call's result does not
+ * vary. */
+int64_t lpq_rmsnorm_backward_workspace(int64_t M, int64_t N);   /* 0 for an invalid shape */
+lpq_status lpq_rmsnorm_backward(const uint16_t* dy, const uint16_t* h, const uint16_t* gamma, const float* rstd,
+                                const uint16_t* dres, int64_t M, int64_t N, uint16_t* dx, float* dgamma, int accumulate,
+                                void* workspace, int64_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

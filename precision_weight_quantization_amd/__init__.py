@@ -12,6 +12,7 @@ If the library has not been built the import fails: there is no fallback.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -83,6 +84,10 @@ _SIG = {
     "lpq_mxfp4_qdq_floor_grouped": (_int, [_tp, _vp, _i32, _vp]),
     "lpq_quantize_mxfp8_transposed": (_int, [_vp, _i64, _i64, _int, _vp, _vp, _vp, _vp, _vp]),
     "lpq_quantize_mxfp4_transposed": (_int, [_vp, _i64, _i64, _int, _vp, _vp, _vp, _vp, _vp]),
+    "lpq_rmsnorm": (_int, [_vp, _vp, _vp, ctypes.c_float, _i64, _i64, _vp, _vp, _vp, _vp]),
+    "lpq_rmsnorm_mxfp8": (_int, [_vp, _vp, _vp, ctypes.c_float, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _vp]),
+    "lpq_rmsnorm_backward_workspace": (_i64, [_i64, _i64]),
+    "lpq_rmsnorm_backward": (_int, [_vp, _vp, _vp, _vp, _vp, _i64, _i64, _vp, _vp, _int, _vp, _i64, _vp]),
     "lpq_nvfp4_global_scale_reciprocal": (_int, [_vp, _i32, _vp, _vp]),
     "lpq_nvfp4_global_scale": (_int, [_vp, _i32, _vp, _vp]),
     "lpq_quantize_nvfp4_ex": (_int, [_vp, _i64, _i64, _vp, _int, _vp, _vp, _vp, _vp]),
@@ -147,6 +152,17 @@ def _launch(fn, where: str, like, stream, *args) -> None:
     else:
         with torch.cuda.device(index):
             _check(fn(*args, _stream(stream)), where)
+
+
+_HERE = contextlib.nullcontext()
+
+
+def _on(stream):
+    """Where a call allocates what it is not given: on the stream that it launches on, so
+    that the memory's earlier users are ordered before it and its later ones behind it."""
+    if stream is None:
+        return _HERE
+    return torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream)))
 
 
 def _ptr(t) -> int:
@@ -284,9 +300,10 @@ def lpq_dequantize_mxfp8(q, e, y=None, stream=None):
 def _mxfp4_quantize(fn, where, w, p, e, stream):
     w = _bf16_in(w, "w")
     M, N = w.shape
-    p, e = _outs(w, (p, "p", M * (N // 2), (M, max(N // 2, 1)), torch.uint8, 1),
-                 (e, "e", M * (N // 32), (M, max(N // 32, 1)), torch.uint8, 1))
-    _check(fn(w.data_ptr(), M, N, p.data_ptr(), e.data_ptr(), _stream(stream)), where)
+    with _on(stream):
+        p, e = _outs(w, (p, "p", M * (N // 2), (M, max(N // 2, 1)), torch.uint8, 1),
+                     (e, "e", M * (N // 32), (M, max(N // 32, 1)), torch.uint8, 1))
+    _launch(fn, where, w, stream, w.data_ptr(), M, N, p.data_ptr(), e.data_ptr())
     return p, e
 
 
@@ -305,17 +322,18 @@ def lpq_dequantize_mxfp4(p, e, y=None, stream=None):
     p = _codes_in(p, "p")
     M, N = p.shape[0], p.shape[1] * 2
     _arg(e, "e", p, M * (N // 32), esize=1)
-    y = _out(y, "y", p, 2 * M * N, (M, N), torch.bfloat16, 2)
-    _check(_L.lpq_dequantize_mxfp4(p.data_ptr(), e.data_ptr(), M, N, y.data_ptr(), _stream(stream)),
-           "lpq_dequantize_mxfp4")
+    with _on(stream):
+        y = _out(y, "y", p, 2 * M * N, (M, N), torch.bfloat16, 2)
+    _launch(_L.lpq_dequantize_mxfp4, "lpq_dequantize_mxfp4", p, stream, p.data_ptr(), e.data_ptr(), M, N, y.data_ptr())
     return y
 
 
 def _mxfp4_qdq(fn, where, x, y, stream):
     x = _bf16_in(x, "x")
     M, N = x.shape
-    y = _out(y, "y", x, 2 * M * N, (M, N), torch.bfloat16, 2)
-    _check(fn(x.data_ptr(), M, N, y.data_ptr(), _stream(stream)), where)
+    with _on(stream):
+        y = _out(y, "y", x, 2 * M * N, (M, N), torch.bfloat16, 2)
+    _launch(fn, where, x, stream, x.data_ptr(), M, N, y.data_ptr())
     return y
 
 
@@ -342,7 +360,8 @@ def _mx_transposed(fn, where, per_byte, dtype, w, rows, floor, qt, et, q, e, str
     if rows:
         specs += [(q, "q", M * (N // per_byte), (M, max(N // per_byte, 1)), dtype, 1),
                   (e, "e", M * (N // 32), (M, max(N // 32, 1)), torch.uint8, 1)]
-    qt, et, q, e = (_outs(w, *specs) + [None, None])[:4]
+    with _on(stream):
+        qt, et, q, e = (_outs(w, *specs) + [None, None])[:4]
     _launch(fn, where, w, stream, w.data_ptr(), M, N, int(bool(floor)), _ptr(q), _ptr(e), qt.data_ptr(), et.data_ptr())
     return qt, et, q, e
 
@@ -540,6 +559,90 @@ def lpq_int4_qdq(x, group=128, y=None, stream=None):
     y = _out(y, "y", x, 2 * M * N, (M, N), torch.bfloat16, 2)
     _check(_L.lpq_int4_qdq(x.data_ptr(), M, N, int(group), y.data_ptr(), _stream(stream)), "lpq_int4_qdq")
     return y
+
+
+# --------------------------------------------------------------------------- root-mean-square norm
+
+def _norm_inputs(x, gamma, residual):
+    x = _bf16_in(x, "x")
+    M, N = x.shape
+    _arg(gamma, "gamma", x, 2 * N, dtypes=_BF16)
+    if residual is not None:
+        _arg(residual, "residual", x, 2 * M * N, dtypes=_BF16)
+    return x, M, N
+
+
+def lpq_rmsnorm(x, gamma, eps=1e-6, residual=None, h=None, rstd=None, y=None, stream=None):
+    """BF16 x [M,N] (N % 32 == 0, N <= 32768), gamma [N] -> (y [M,N] BF16, h [M,N] BF16, rstd [M] FP32):
+    the root-mean-square norm of h = x + residual.  Without a residual h is x itself."""
+    x, M, N = _norm_inputs(x, gamma, residual)
+    if residual is None and h is not None:
+        raise ValueError("h is an output of the residual's addition: pass residual with it")
+    specs = [(y, "y", 2 * M * N, (M, N), torch.bfloat16, 2), (rstd, "rstd", 4 * M, (M,), torch.float32, 4)]
+    if residual is not None:
+        specs.append((h, "h", 2 * M * N, (M, N), torch.bfloat16, 2))
+    with _on(stream):
+        y, rstd, h = (_outs(x, *specs) + [None])[:3]
+    _launch(_L.lpq_rmsnorm, "lpq_rmsnorm", x, stream, x.data_ptr(), _ptr(residual), gamma.data_ptr(), float(eps), M, N, _ptr(h),
+            rstd.data_ptr(), y.data_ptr())
+    return y, (x if h is None else h), rstd
+
+
+def lpq_rmsnorm_mxfp8(x, gamma, eps=1e-6, residual=None, h=None, rstd=None, y=None, q=None, e=None, stream=None):
+    """As lpq_rmsnorm, quantized: -> (q [M,N] float8_e4m3fn, e [M,N/32] uint8, h, rstd), the MXFP8 form of y.
+    Pass a BF16 tensor ``y`` to have the unquantized result as well."""
+    x, M, N = _norm_inputs(x, gamma, residual)
+    if residual is None and h is not None:
+        raise ValueError("h is an output of the residual's addition: pass residual with it")
+    if y is not None:
+        _arg(y, "y", x, 2 * M * N, esize=2)
+    specs = [(q, "q", M * N, (M, N), torch.float8_e4m3fn, 1), (e, "e", M * (N // 32), (M, max(N // 32, 1)), torch.uint8, 1),
+             (rstd, "rstd", 4 * M, (M,), torch.float32, 4)]
+    if residual is not None:
+        specs.append((h, "h", 2 * M * N, (M, N), torch.bfloat16, 2))
+    with _on(stream):
+        q, e, rstd, h = (_outs(x, *specs) + [None])[:4]
+    _launch(_L.lpq_rmsnorm_mxfp8, "lpq_rmsnorm_mxfp8", x, stream, x.data_ptr(), _ptr(residual), gamma.data_ptr(), float(eps),
+            M, N, _ptr(h), rstd.data_ptr(), _ptr(y), q.data_ptr(), e.data_ptr())
+    return q, e, (x if h is None else h), rstd
+
+
+def lpq_rmsnorm_backward_workspace(M, N):
+    """Bytes of workspace that lpq_rmsnorm_backward needs for dgamma (0 for a shape it refuses)."""
+    return int(_L.lpq_rmsnorm_backward_workspace(int(M), int(N)))
+
+
+def lpq_rmsnorm_backward(dy, h, gamma, rstd, dres=None, dx=None, dgamma=None, accumulate=False, want_dgamma=True,
+                         workspace=None, stream=None):
+    """Gradients of lpq_rmsnorm (of lpq_rmsnorm_mxfp8 under a straight-through estimator) from its h and rstd:
+    (dx [M,N] BF16, of x and of residual alike, with dres [M,N] added; dgamma [N] FP32, None without
+    ``want_dgamma``).  accumulate: add to the ``dgamma`` passed in.  workspace: a device tensor of at least
+    lpq_rmsnorm_backward_workspace(M, N) bytes, used by one call at a time; allocated when not given."""
+    dy = _bf16_in(dy, "dy")
+    M, N = dy.shape
+    for t, name in ((h, "h"), (dres, "dres")):
+        if t is not None or name == "h":
+            _arg(t, name, dy, 2 * M * N, dtypes=_BF16)
+    _arg(gamma, "gamma", dy, 2 * N, dtypes=_BF16)
+    _f32_words(rstd, "rstd", dy, M)
+    if accumulate and dgamma is None:
+        raise ValueError("accumulate adds to a dgamma that is passed in")
+    if dgamma is not None and not want_dgamma:
+        raise ValueError("dgamma was passed in, and want_dgamma is False")
+    need = lpq_rmsnorm_backward_workspace(M, N) if want_dgamma else 0
+    if workspace is not None:
+        _arg(workspace, "workspace", dy, need)
+    specs = [(dx, "dx", 2 * M * N, (M, N), torch.bfloat16, 2)]
+    if want_dgamma:
+        specs.append((dgamma, "dgamma", 4 * N, (N,), torch.float32, 4))
+    with _on(stream):
+        dx, dgamma = (_outs(dy, *specs) + [None])[:2]
+        if need and workspace is None:
+            workspace = _empty((need,), torch.uint8, dy)
+    _launch(_L.lpq_rmsnorm_backward, "lpq_rmsnorm_backward", dy, stream, dy.data_ptr(), h.data_ptr(), gamma.data_ptr(),
+            rstd.data_ptr(), _ptr(dres), M, N, dx.data_ptr(), _ptr(dgamma), int(bool(accumulate)), _ptr(workspace),
+            0 if workspace is None else workspace.numel() * workspace.element_size())
+    return dx, dgamma
 
 
 # --------------------------------------------------------------------------- FP8 re-quantization

@@ -52,6 +52,7 @@ using namespace lpq;
 #include "lpq_fp8blk.hpp"
 #include "lpq_requant.hpp"
 #include "lpq_mx_transpose.hpp"
+#include "lpq_rmsnorm.hpp"
 
 
 // ===========================================================================
@@ -583,6 +584,80 @@ lpq_status mx_transpose(const uint16_t* w, int64_t M, int64_t N, int floor_rule,
     return launched();
 }
 
+// Shape of a norm call: whole MXFP8 blocks, a row that fits the kernels' registers.
+lpq_status norm_shape(int64_t M, int64_t N) {
+    if (M <= 0 || N <= 0 || N % 32 || N > kNormMaxN || M > (int64_t(1) << 40) / N) return LPQ_ERR_SHAPE;
+    return LPQ_OK;
+}
+
+lpq_status rmsnorm(const NormArgs& A, void* stream) {
+    lpq_status st = norm_shape(A.M, A.N);
+    if (st != LPQ_OK) return st;
+    if (!A.x || !A.gamma || (!A.y && !A.q) || !A.q != !A.e || (A.residual && !A.h)) return LPQ_ERR_NULL;
+    if (!A.residual && A.h) return LPQ_ERR_ARG;   // without a residual h is x
+    if (!(A.eps > 0.0f) || A.eps > 3.4028235e38f) return LPQ_ERR_ARG;
+    if (!aligned(A.x, 16) || !aligned(A.residual, 16) || !aligned(A.gamma, 16) || !aligned(A.h, 16) || !aligned(A.y, 16) ||
+        !aligned(A.q, 8) || !aligned(A.rstd, 4))
+        return LPQ_ERR_ALIGN;
+    const int64_t n = A.M * A.N;
+    const struct { const void* p; int64_t n; } in[] = {{A.x, 2 * n}, {A.residual, A.residual ? 2 * n : 0}, {A.gamma, 2 * (int64_t)A.N}},
+        out[] = {{A.h, A.h ? 2 * n : 0}, {A.y, A.y ? 2 * n : 0}, {A.q, A.q ? n : 0}, {A.e, A.e ? n / 32 : 0}, {A.rstd, A.rstd ? 4 * A.M : 0}};
+    for (int i = 0; i < 5; i++) {
+        for (int j = 0; j < 3; j++)   // h may be x or the residual itself: a lane reads what it writes first
+            if (!(i == 0 && j < 2 && in[j].p == out[i].p) && overlap(out[i].p, out[i].n, in[j].p, in[j].n)) return LPQ_ERR_ARG;
+        for (int j = 0; j < i; j++)
+            if (overlap(out[i].p, out[i].n, out[j].p, out[j].n)) return LPQ_ERR_ARG;
+    }
+    return by_row(A.N, [&](auto shape) {
+        constexpr int G = decltype(shape)::g, U = decltype(shape)::u, kRows = norm_threads(G) / G;
+        const int64_t groups = (A.M + kRows - 1) / kRows;
+        if (groups > kMaxGridX) return LPQ_ERR_SHAPE;
+        hipLaunchKernelGGL((k_rmsnorm<G, U>), dim3((unsigned)groups), dim3(norm_threads(G)), 0, (hipStream_t)stream, A);
+        return launched();
+    });
+}
+
+// Workgroups of the backward pass: at most LPQ_NORMG_GROUPS, each with a
+// partial sum of dgamma.
+int64_t norm_grad_groups(int64_t M, int64_t N) {
+    return by_row(N, [&](auto shape) {
+        constexpr int G = decltype(shape)::g, kRows = norm_threads(G) / G;
+        const int64_t groups = (M + kRows - 1) / kRows, most = LPQ_NORMG_GROUPS;
+        return groups < most ? groups : most;
+    });
+}
+
+lpq_status rmsnorm_grad(NormGradArgs A, float* dgamma, int accumulate, void* workspace, int64_t workspace_bytes, void* stream) {
+    lpq_status st = norm_shape(A.M, A.N);
+    if (st != LPQ_OK) return st;
+    if (!A.dy || !A.h || !A.gamma || !A.rstd || !A.dx || (dgamma && !workspace)) return LPQ_ERR_NULL;
+    if (!aligned(A.dy, 16) || !aligned(A.h, 16) || !aligned(A.gamma, 16) || !aligned(A.dres, 16) || !aligned(A.dx, 16) ||
+        !aligned(A.rstd, 4) || !aligned(dgamma, 4) || !aligned(workspace, 16))
+        return LPQ_ERR_ALIGN;
+    const int64_t n = A.M * A.N, groups = norm_grad_groups(A.M, A.N), need = dgamma ? 4 * groups * A.N : 0;
+    if (workspace_bytes < need) return LPQ_ERR_ARG;
+    const struct { const void* p; int64_t n; } in[] = {{A.dy, 2 * n}, {A.dres, A.dres ? 2 * n : 0}, {A.h, 2 * n},
+                                                       {A.gamma, 2 * (int64_t)A.N}, {A.rstd, 4 * A.M}},
+        out[] = {{A.dx, 2 * n}, {dgamma, dgamma ? 4 * (int64_t)A.N : 0}, {workspace, need}};
+    for (int i = 0; i < 3; i++) {
+        for (int j = 0; j < 5; j++)   // dx may be dy or dres itself
+            if (!(i == 0 && j < 2 && in[j].p == out[i].p) && overlap(out[i].p, out[i].n, in[j].p, in[j].n)) return LPQ_ERR_ARG;
+        for (int j = 0; j < i; j++)
+            if (overlap(out[i].p, out[i].n, out[j].p, out[j].n)) return LPQ_ERR_ARG;
+    }
+    A.part = dgamma ? static_cast<float*>(workspace) : nullptr;
+    const hipStream_t s = (hipStream_t)stream;
+    st = by_row(A.N, [&](auto shape) {
+        constexpr int G = decltype(shape)::g, U = decltype(shape)::u;
+        hipLaunchKernelGGL((k_rmsnorm_grad<G, U>), dim3((unsigned)groups), dim3(norm_threads(G)), 0, s, A);
+        return launched();
+    });
+    if (st != LPQ_OK || !dgamma) return st;
+    hipLaunchKernelGGL(k_rmsnorm_dgamma, dim3((unsigned)((A.N + kDgCols - 1) / kDgCols)), dim3(kDgCols * kDgSlices), 0, s, A.part,
+                       (int32_t)groups, A.N, accumulate, dgamma);
+    return launched();
+}
+
 // Host-side checks of an observer call; the workgroup count on success.
 lpq_status observe_args(const uint16_t* x, int64_t M, int64_t N, int observer, const float* state, const float* amax,
                         lpq_tensor* one, int64_t* units) {
@@ -738,6 +813,31 @@ lpq_status lpq_quantize_mxfp8_transposed(const uint16_t* w, int64_t M, int64_t N
 lpq_status lpq_quantize_mxfp4_transposed(const uint16_t* w, int64_t M, int64_t N, int floor_rule, uint8_t* p, uint8_t* e,
                                          uint8_t* pt, uint8_t* et, void* stream) {
     return mx_transpose<true>(w, M, N, floor_rule, p, e, pt, et, stream);
+}
+
+lpq_status lpq_rmsnorm(const uint16_t* x, const uint16_t* residual, const uint16_t* gamma, float eps, int64_t M, int64_t N,
+                       uint16_t* h, float* rstd, uint16_t* y, void* stream) {
+    if (N <= 0 || N > kNormMaxN) return LPQ_ERR_SHAPE;
+    return rmsnorm(NormArgs{x, residual, gamma, h, y, rstd, nullptr, nullptr, M, (int32_t)N, eps}, stream);
+}
+
+lpq_status lpq_rmsnorm_mxfp8(const uint16_t* x, const uint16_t* residual, const uint16_t* gamma, float eps, int64_t M, int64_t N,
+                             uint16_t* h, float* rstd, uint16_t* y, uint8_t* q, uint8_t* e, void* stream) {
+    if (N <= 0 || N > kNormMaxN) return LPQ_ERR_SHAPE;
+    if (!q || !e) return LPQ_ERR_NULL;
+    return rmsnorm(NormArgs{x, residual, gamma, h, y, rstd, q, e, M, (int32_t)N, eps}, stream);
+}
+
+int64_t lpq_rmsnorm_backward_workspace(int64_t M, int64_t N) {
+    return norm_shape(M, N) == LPQ_OK ? 4 * norm_grad_groups(M, N) * N : 0;
+}
+
+lpq_status lpq_rmsnorm_backward(const uint16_t* dy, const uint16_t* h, const uint16_t* gamma, const float* rstd,
+                                const uint16_t* dres, int64_t M, int64_t N, uint16_t* dx, float* dgamma, int accumulate,
+                                void* workspace, int64_t workspace_bytes, void* stream) {
+    if (N <= 0 || N > kNormMaxN) return LPQ_ERR_SHAPE;
+    return rmsnorm_grad(NormGradArgs{dy, h, gamma, dres, rstd, dx, nullptr, M, (int32_t)N}, dgamma, accumulate, workspace,
+                        workspace_bytes, stream);
 }
 
 lpq_status lpq_nvfp4_global_scale_reciprocal(const float* group_amax, int32_t n_groups, float* out, void* stream) {

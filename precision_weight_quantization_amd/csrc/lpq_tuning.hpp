@@ -195,3 +195,7 @@
 #ifndef LPQ_MX4QDQ_AHEAD
 #define LPQ_MX4QDQ_AHEAD 1
 #endif
+// Workgroups of the norm's backward pass, each with a partial sum of dgamma.
+#ifndef LPQ_NORMG_GROUPS
+#define LPQ_NORMG_GROUPS 512
+#endif

@@ -87,3 +87,81 @@ def test_transposed_binding(lib, recorder):
         with pytest.raises(exc):
             call()
     assert recorder.calls == []
+
+
+def test_rmsnorm_validation(lib):
+    L = lib.raw()
+    Q = [P + (i << 24) for i in range(12)]   # ranges that do not meet
+    x, res, gm, h, rs, y, q, e = Q[:8]
+    f, fq = L.lpq_rmsnorm, L.lpq_rmsnorm_mxfp8
+    assert f(None, None, gm, 1e-6, 4, 64, None, rs, y, None) == 1
+    assert f(x, None, None, 1e-6, 4, 64, None, rs, y, None) == 1
+    assert f(x, None, gm, 1e-6, 4, 64, None, rs, None, None) == 1
+    assert f(x, res, gm, 1e-6, 4, 64, None, rs, y, None) == 1            # the sum needs a place
+    assert f(x, None, gm, 1e-6, 4, 64, h, rs, y, None) == 6              # h without a residual
+    assert f(x, None, gm, 1e-6, 0, 64, None, rs, y, None) == 2
+    assert f(x, None, gm, 1e-6, 4, 48, None, rs, y, None) == 2
+    assert f(x, None, gm, 1e-6, 4, 32800, None, rs, y, None) == 2
+    assert f(x, None, gm, 1e-6, 4, 64 + (1 << 32), None, rs, y, None) == 2
+    assert f(x, None, gm, 1e-6, 1 << 40, 64, None, rs, y, None) == 2
+    for eps in (0.0, -1e-6, float("inf"), float("nan")):
+        assert f(x, None, gm, eps, 4, 64, None, rs, y, None) == 6
+    assert f(x + 8, None, gm, 1e-6, 4, 64, None, rs, y, None) == 3
+    assert f(x, None, gm + 8, 1e-6, 4, 64, None, rs, y, None) == 3
+    assert f(x, res + 2, gm, 1e-6, 4, 64, h, rs, y, None) == 3
+    assert f(x, None, gm, 1e-6, 4, 64, None, rs + 2, y, None) == 3
+    assert f(x, None, gm, 1e-6, 4, 64, None, rs, x, None) == 6           # y over x
+    assert f(x, res, gm, 1e-6, 4, 64, x + 64, rs, y, None) == 6          # h over a part of x
+    assert f(x, res, gm, 1e-6, 4, 64, h, rs, h + 16, None) == 6
+    assert f(x, None, gm, 1e-6, 4, 64, None, gm, y, None) == 6           # rstd over gamma
+    assert fq(x, None, gm, 1e-6, 4, 64, None, rs, None, None, e, None) == 1
+    assert fq(x, None, gm, 1e-6, 4, 64, None, rs, None, q, None, None) == 1
+    assert fq(x, None, gm, 1e-6, 4, 64, None, rs, None, q + 4, e, None) == 3
+    assert fq(x, None, gm, 1e-6, 4, 64, None, rs, None, q, q + 128, None) == 6
+    b = L.lpq_rmsnorm_backward
+    dy, hh, g2, r2, dr, dx, dg, ws = Q[:8]
+    need = L.lpq_rmsnorm_backward_workspace(1000, 64)
+    assert need > 0 and need % 256 == 0
+    assert L.lpq_rmsnorm_backward_workspace(0, 64) == 0
+    assert L.lpq_rmsnorm_backward_workspace(4, 40) == 0
+    ok = [dy, hh, g2, r2, dr, 1000, 64, dx, dg, 0, ws, need, None]
+
+    def call(**change):
+        a = list(ok)
+        for k, v in change.items():
+            a["dy h gamma rstd dres M N dx dgamma accumulate ws bytes stream".split().index(k)] = v
+        return b(*a)
+
+    for k in ("dy", "h", "gamma", "rstd", "dx", "ws"):
+        assert call(**{k: None}) == 1, k
+    assert call(M=0) == 2 and call(N=48) == 2 and call(N=40000) == 2
+    assert call(bytes=need - 1) == 6
+    for k, v in (("dy", dy + 8), ("h", hh + 8), ("gamma", g2 + 2), ("rstd", r2 + 2), ("dres", dr + 8), ("dx", dx + 8),
+                 ("dgamma", dg + 2), ("ws", ws + 8)):
+        assert call(**{k: v}) == 3, k
+    assert call(dx=hh) == 6 and call(dx=dy + 64) == 6 and call(dgamma=ws) == 6 and call(ws=dx + 1024) == 6
+    assert L.lpq_last_hip_error() == 0
+
+
+def test_rmsnorm_binding(lib, recorder):
+    bf = lambda *s: fake(torch.zeros(s, dtype=torch.bfloat16))
+    u8 = lambda *s: fake(torch.zeros(s, dtype=torch.uint8))
+    f32 = lambda *s: fake(torch.zeros(s, dtype=torch.float32))
+    x, g = bf(4, 64), bf(64)
+    for exc, call in [
+            (TypeError, lambda: lib.lpq_rmsnorm(f32(4, 64), g)),
+            (ValueError, lambda: lib.lpq_rmsnorm(x, bf(63))),
+            (TypeError, lambda: lib.lpq_rmsnorm(x, f32(64))),
+            (ValueError, lambda: lib.lpq_rmsnorm(x, g, residual=bf(4, 32))),
+            (ValueError, lambda: lib.lpq_rmsnorm(x, g, h=bf(4, 64))),
+            (ValueError, lambda: lib.lpq_rmsnorm(x, g, rstd=f32(3))),
+            (ValueError, lambda: lib.lpq_rmsnorm_mxfp8(x, g, q=u8(4, 63))),
+            (ValueError, lambda: lib.lpq_rmsnorm_mxfp8(x, g, y=bf(4, 63))),
+            (ValueError, lambda: lib.lpq_rmsnorm_backward(x, bf(3, 64), g, f32(4))),
+            (ValueError, lambda: lib.lpq_rmsnorm_backward(x, x, g, f32(3))),
+            (ValueError, lambda: lib.lpq_rmsnorm_backward(x, x, g, f32(4), accumulate=True)),
+            (ValueError, lambda: lib.lpq_rmsnorm_backward(x, x, g, f32(4), dgamma=f32(64), want_dgamma=False)),
+            (ValueError, lambda: lib.lpq_rmsnorm_backward(x, x, g, f32(4), dgamma=f32(63)))]:
+        with pytest.raises(exc):
+            call()
+    assert [c for c in recorder.calls if c != "lpq_rmsnorm_backward_workspace"] == []
