@@ -521,6 +521,31 @@ lpq_status lpq_rmsnorm_backward(const uint16_t* dy, const uint16_t* h, const uin
                                 const uint16_t* dres, int64_t M, int64_t N, uint16_t* dx, float* dgamma, int accumulate,
                                 void* workspace, int64_t workspace_bytes, void* stream);
 
+/* ======================================================================== */
+/* The product of two microscaled matrices, contracted along their blocks:
+ *   y[m, n] = sum over k of a[m, k] * b[n, k]
+ * a [M, K]: activations (or a gradient), b [N, K]: weights (or the other
+ * operand), each MXFP8 (codes [., K]) or MXFP4 (packed [., K/2]) with scale
+ * bytes ae [M, K/32], be [N, K/32], as the quantizers above write them.  K % 32
+ * == 0; any M and N; each below 2^31 - 1024, no operand or result above 2^40
+ * elements.  Codes and y 16-byte aligned, scale bytes any.
+ * y [M, N]: LPQ_BF16, or LPQ_F32 when both operands are MXFP4 (the matrix
+ * instruction sums E2M1 products exactly; with an E4M3 operand it drops what
+ * lies about 2^-16 below the largest product of 128, so that an FP32 result is
+ * refused: LPQ_ERR_ARG).  y may not overlap an input (LPQ_ERR_ARG).
+ * Every sum is FP32 in a fixed order: a call's result does not vary.
+ * NaN codes (0x7F, 0xFF) and scale byte 255 are outside the contract.
+ * A layer's three products: forward y = x w^T (a = x, b = w, both in row form),
+ * dx = dy w (a = dy, b = w transposed), dw = dy^T x (a = dy transposed, b = x
+ * transposed), the transposed forms from lpq_quantize_mxfp8_transposed /
+ * lpq_quantize_mxfp4_transposed. */
+#define LPQ_MXFP8 0
+#define LPQ_MXFP4 1
+#define LPQ_BF16 0
+#define LPQ_F32 1
+lpq_status lpq_mx_matmul(const uint8_t* a, const uint8_t* ae, int a_format, const uint8_t* b, const uint8_t* be, int b_format,
+                         int64_t M, int64_t N, int64_t K, void* y, int y_type, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -88,6 +88,7 @@ _SIG = {
     "lpq_rmsnorm_mxfp8": (_int, [_vp, _vp, _vp, ctypes.c_float, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _vp]),
     "lpq_rmsnorm_backward_workspace": (_i64, [_i64, _i64]),
     "lpq_rmsnorm_backward": (_int, [_vp, _vp, _vp, _vp, _vp, _i64, _i64, _vp, _vp, _int, _vp, _i64, _vp]),
+    "lpq_mx_matmul": (_int, [_vp, _vp, _int, _vp, _vp, _int, _i64, _i64, _i64, _vp, _int, _vp]),
     "lpq_nvfp4_global_scale_reciprocal": (_int, [_vp, _i32, _vp, _vp]),
     "lpq_nvfp4_global_scale": (_int, [_vp, _i32, _vp, _vp]),
     "lpq_quantize_nvfp4_ex": (_int, [_vp, _i64, _i64, _vp, _int, _vp, _vp, _vp, _vp]),
@@ -643,6 +644,45 @@ def lpq_rmsnorm_backward(dy, h, gamma, rstd, dres=None, dx=None, dgamma=None, ac
             rstd.data_ptr(), _ptr(dres), M, N, dx.data_ptr(), _ptr(dgamma), int(bool(accumulate)), _ptr(workspace),
             0 if workspace is None else workspace.numel() * workspace.element_size())
     return dx, dgamma
+
+
+# --------------------------------------------------------------------------- microscaled products
+
+MX_FORMATS = {"mxfp8": 0, "mxfp4": 1}
+_MX_OUT = {torch.bfloat16: 0, torch.float32: 1}
+
+
+def _mx_operand(codes, scales, fmt, name, like=None):
+    """(format, rows, columns) of a microscaled operand, from its format's name or its codes' dtype."""
+    _arg(codes, name, like, esize=1, dims=2)
+    if fmt is None:
+        if codes.dtype not in (torch.float8_e4m3fn, torch.uint8):
+            raise TypeError(f"{name} holds float8_e4m3fn codes (MXFP8) or uint8 (packed MXFP4), got {codes.dtype}")
+        fmt = "mxfp8" if codes.dtype == torch.float8_e4m3fn else "mxfp4"
+    elif fmt not in MX_FORMATS:
+        raise ValueError(f"the format of {name} is one of {sorted(MX_FORMATS)}, got {fmt!r}")
+    rows, cols = codes.shape
+    cols *= 2 if fmt == "mxfp4" else 1
+    _arg(scales, name + "e", codes, rows * (cols // 32), esize=1)
+    return MX_FORMATS[fmt], rows, cols
+
+
+def lpq_mx_matmul(a, ae, b, be, out_dtype=torch.bfloat16, y=None, a_format=None, b_format=None, stream=None):
+    """y [M,N] = a b^T of two microscaled matrices: a [M,K] and b [N,K] codes with UE8M0 scale bytes ae
+    [M,K/32] and be [N,K/32].  float8_e4m3fn codes are MXFP8, uint8 codes packed MXFP4, unless ``a_format`` /
+    ``b_format`` ("mxfp8", "mxfp4") say otherwise.  out_dtype: bfloat16, or float32 when both are MXFP4."""
+    fa, M, K = _mx_operand(a, ae, a_format, "a")
+    fb, N, Kb = _mx_operand(b, be, b_format, "b", a)
+    if K != Kb:
+        raise ValueError(f"a has {K} columns, b {Kb}")
+    if out_dtype not in _MX_OUT:
+        raise TypeError(f"out_dtype must be one of {[str(d) for d in _MX_OUT]}, got {out_dtype}")
+    size = 4 if out_dtype == torch.float32 else 2
+    with _on(stream):
+        y = _out(y, "y", a, size * M * N, (M, N), out_dtype, size)
+    _launch(_L.lpq_mx_matmul, "lpq_mx_matmul", a, stream, a.data_ptr(), ae.data_ptr(), fa, b.data_ptr(), be.data_ptr(), fb,
+            M, N, K, y.data_ptr(), _MX_OUT[out_dtype])
+    return y
 
 
 # --------------------------------------------------------------------------- FP8 re-quantization

@@ -35,6 +35,7 @@
 #include <stdint.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "lpq.h"
 #include "lpq_device.hpp"
@@ -53,6 +54,7 @@ using namespace lpq;
 #include "lpq_requant.hpp"
 #include "lpq_mx_transpose.hpp"
 #include "lpq_rmsnorm.hpp"
+#include "lpq_mx_matmul.hpp"
 
 
 // ===========================================================================
@@ -658,6 +660,21 @@ lpq_status rmsnorm_grad(NormGradArgs A, float* dgamma, int accumulate, void* wor
     return launched();
 }
 
+template <bool FP4A, bool FP4B>
+lpq_status mx_matmul(const MatmulArgs& A, hipStream_t s) {
+    const int tiles_n = (A.N + 15) / 16;
+    auto rows = [&](auto mt) {
+        constexpr int MT = decltype(mt)::value;
+        const int64_t grid = ((int64_t)A.M + 16 * MT - 1) / (16 * MT) * tiles_n;
+        if (grid > kMaxGridX) return LPQ_ERR_SHAPE;
+        hipLaunchKernelGGL((k_mx_matmul_rows<FP4B, FP4A, MT>), dim3((unsigned)grid), dim3(64 * kRowsWaves), 0, s, A, tiles_n);
+        return launched();
+    };
+    if (A.M <= 16) return rows(std::integral_constant<int, 1>{});
+    if (A.M <= 32) return rows(std::integral_constant<int, 2>{});
+    return rows(std::integral_constant<int, 4>{});
+}
+
 // Host-side checks of an observer call; the workgroup count on success.
 lpq_status observe_args(const uint16_t* x, int64_t M, int64_t N, int observer, const float* state, const float* amax,
                         lpq_tensor* one, int64_t* units) {
@@ -838,6 +855,26 @@ lpq_status lpq_rmsnorm_backward(const uint16_t* dy, const uint16_t* h, const uin
     if (N <= 0 || N > kNormMaxN) return LPQ_ERR_SHAPE;
     return rmsnorm_grad(NormGradArgs{dy, h, gamma, dres, rstd, dx, nullptr, M, (int32_t)N}, dgamma, accumulate, workspace,
                         workspace_bytes, stream);
+}
+
+lpq_status lpq_mx_matmul(const uint8_t* a, const uint8_t* ae, int a_format, const uint8_t* b, const uint8_t* be, int b_format,
+                         int64_t M, int64_t N, int64_t K, void* y, int y_type, void* stream) {
+    const int64_t most = (int64_t(1) << 31) - 1024;   // tile and element offsets inside a row stay 32-bit
+    if (M <= 0 || N <= 0 || K <= 0 || K % 32 || M > most || N > most || K > most) return LPQ_ERR_SHAPE;
+    if (M > (int64_t(1) << 40) / N || M > (int64_t(1) << 40) / K || N > (int64_t(1) << 40) / K) return LPQ_ERR_SHAPE;
+    if (!a || !ae || !b || !be || !y) return LPQ_ERR_NULL;
+    const bool a4 = a_format == LPQ_MXFP4, b4 = b_format == LPQ_MXFP4;
+    if ((!a4 && a_format != LPQ_MXFP8) || (!b4 && b_format != LPQ_MXFP8)) return LPQ_ERR_ARG;
+    if (y_type != LPQ_BF16 && !(y_type == LPQ_F32 && a4 && b4)) return LPQ_ERR_ARG;
+    if (!aligned(a, 16) || !aligned(b, 16) || !aligned(y, 16)) return LPQ_ERR_ALIGN;
+    const int64_t ny = M * N * (y_type == LPQ_F32 ? 4 : 2);
+    if (overlap(y, ny, a, M * K / (a4 ? 2 : 1)) || overlap(y, ny, ae, M * K / 32) || overlap(y, ny, b, N * K / (b4 ? 2 : 1)) ||
+        overlap(y, ny, be, N * K / 32))
+        return LPQ_ERR_ARG;
+    const MatmulArgs A{a, ae, b, be, y, (int32_t)M, (int32_t)N, (int32_t)K, y_type == LPQ_F32};
+    const hipStream_t s = (hipStream_t)stream;
+    if (a4) return b4 ? mx_matmul<true, true>(A, s) : mx_matmul<true, false>(A, s);
+    return b4 ? mx_matmul<false, true>(A, s) : mx_matmul<false, false>(A, s);
 }
 
 lpq_status lpq_nvfp4_global_scale_reciprocal(const float* group_amax, int32_t n_groups, float* out, void* stream) {

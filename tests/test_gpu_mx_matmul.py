@@ -1,0 +1,134 @@
+"""Products of microscaled matrices against 64-bit products of the numbers that the
+codes stand for.
+
+Tolerances.  Let S = sum over k of |a b|.  Two E2M1 operands: the instruction's sum of
+128 products is exact up to one FP32 rounding of the running sum, at most K/128 steps
+and 8 additions of parts: (K/128 + 8) 2^-24 S.  With an E4M3 operand each step also
+drops what lies 2^-16 below its largest product: 128 products, each by at most 2^-16 of
+the step's largest one; the test's bound takes the sum over the steps of 128 2^-16 times
+that largest product (a bound that no summation order can pass).  A BF16 result adds
+half a step of BF16, 2^-8 of the value."""
+import numpy as np
+import pytest
+import torch
+
+from tests import mx_ref as R
+from tests.gpu_util import DEV
+
+pytestmark = pytest.mark.gpu
+
+SHAPES = [(1, 1, 32), (1, 16, 128), (1, 2560, 2560), (3, 17, 96), (5, 130, 160), (16, 64, 256), (17, 33, 1056), (32, 48, 2048),
+          (33, 100, 64), (64, 257, 4128), (65, 96, 512), (77, 2053, 1056), (128, 128, 128), (129, 255, 384), (256, 512, 2560),
+          (300, 260, 1440), (511, 513, 320), (1024, 768, 2048), (700, 1030, 992)]
+FORMATS = [(R.FP8, R.FP8), (R.FP8, R.FP4), (R.FP4, R.FP8), (R.FP4, R.FP4)]
+
+
+@pytest.fixture(scope="module")
+def lpq():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    import precision_weight_quantization_amd as m
+    return m
+
+
+def operand(rows, K, fmt, seed, scale=1.0, outliers=1e-3):
+    """(codes as held, scale bytes, 64-bit values) of seeded normal data, some far out."""
+    rng = np.random.default_rng(seed)
+    x = rng.standard_normal((rows, K)) * scale
+    x = np.where(rng.random((rows, K)) < outliers, x * 50, x)
+    codes, e = R.quantize(R.bf16_to_f64(R.f64_to_bf16(x)), fmt)
+    held = R.pack(codes) if fmt == R.FP4 else codes
+    t = torch.from_numpy(held).to(DEV)
+    return (t if fmt == R.FP4 else t.view(torch.float8_e4m3fn)), torch.from_numpy(e).to(DEV), R.values(codes, e, fmt)
+
+
+def bound(va, vb, exact, fmts, f32):
+    K = va.shape[1]
+    tol = (K / 128 + 8) * 2.0 ** -24 * (np.abs(va) @ np.abs(vb).T)
+    if R.FP8 in fmts:
+        for k in range(0, K, 128):
+            top = np.abs(va[:, k:k + 128]).max(1)[:, None] * np.abs(vb[:, k:k + 128]).max(1)[None, :]
+            tol += 128 * 2.0 ** -16 * top
+    return tol if f32 else tol + 2.0 ** -8 * (np.abs(exact) + tol)
+
+
+def check(lpq, A, B, fmts, f32, **kw):
+    (a, ae, va), (b, be, vb) = A, B
+    y = lpq.lpq_mx_matmul(a, ae, b, be, out_dtype=torch.float32 if f32 else torch.bfloat16, **kw)
+    exact = va @ vb.T
+    err = np.abs(y.double().cpu().numpy() - exact)
+    tol = bound(va, vb, exact, fmts, f32)
+    assert np.isfinite(err).all() and (err <= tol).all(), (err.max(), (err / np.maximum(tol, 1e-300)).max())
+    # over many results far nearer than the worst case: BF16's error is 2^-9 on average
+    rel = np.linalg.norm(err) / max(np.linalg.norm(exact), 1e-300)
+    print(f"  relative error {rel:.3g}", flush=True)
+    assert exact.size < 256 or rel <= (1e-6 if f32 else 2.0 ** -8)
+    return y
+
+
+@pytest.mark.parametrize("fmts", FORMATS)
+@pytest.mark.parametrize("shape", SHAPES)
+def test_shapes(lpq, shape, fmts):
+    M, N, K = shape
+    A, B = operand(M, K, fmts[0], 1), operand(N, K, fmts[1], 2, 0.02, 0.0)
+    print(f"  {shape} {fmts}", flush=True)
+    y = check(lpq, A, B, fmts, False)
+    again = lpq.lpq_mx_matmul(A[0], A[1], B[0], B[1])
+    assert torch.equal(y.view(torch.int16), again.view(torch.int16))
+    if fmts == (R.FP4, R.FP4):
+        check(lpq, A, B, fmts, True)
+
+
+@pytest.mark.parametrize("fmts", FORMATS)
+def test_exact_integers(lpq, fmts):
+    """Small whole numbers under unit scales: every product and sum is exact, so the BF16
+    result is the correctly rounded one, at sizes that end inside every tile."""
+    rng = np.random.default_rng(3)
+    for M, N, K in ((1, 40, 96), (19, 70, 416), (150, 300, 288), (260, 520, 160)):
+        out, vals = [], []
+        for rows, fmt in ((M, fmts[0]), (N, fmts[1])):
+            v = rng.integers(-1, 2, (rows, K)).astype(np.float64)
+            codes = R.nearest_code(v, fmt)
+            held = torch.from_numpy(R.pack(codes) if fmt == R.FP4 else codes).to(DEV)
+            out += [held, torch.full((rows, K // 32), 127, dtype=torch.uint8, device=DEV)]
+            vals.append(v)
+        fm = dict(a_format=fmts[0], b_format=fmts[1])
+        y = lpq.lpq_mx_matmul(*out, **fm)
+        want = R.bf16_to_f64(R.f64_to_bf16(vals[0] @ vals[1].T))
+        assert np.array_equal(y.double().cpu().numpy(), want)
+
+
+@pytest.mark.parametrize("fmts", FORMATS)
+def test_scales_and_zero_blocks(lpq, fmts):
+    """Scales far apart from block to block, blocks of zeros under the smallest scale byte, and a row
+    that is zero everywhere: its results are zeros."""
+    M, N, K = 40, 72, 544
+    res = []
+    for rows, fmt, seed in ((M, fmts[0], 4), (N, fmts[1], 5)):
+        codes, e, _ = operand(rows, K, fmt, seed, 1.0, 0.0)
+        e = e.cpu().numpy().astype(np.int64) + np.random.default_rng(seed).integers(-30, 31, (rows, K // 32))
+        held = codes.view(torch.uint8).cpu().numpy().copy()
+        w = held.reshape(rows, K // 32, -1)
+        w[3] = 0
+        e[3] = 0
+        w[:, 4] = 0
+        e[:, 4] = 0
+        raw = R.unpack(held) if fmt == R.FP4 else held
+        e = e.astype(np.uint8)
+        t = torch.from_numpy(held).to(DEV)
+        res.append((t if fmt == R.FP4 else t.view(torch.float8_e4m3fn), torch.from_numpy(e).to(DEV), R.values(raw, e, fmt)))
+    (a, ae, va), (b, be, vb) = res
+    y = lpq.lpq_mx_matmul(a, ae, b, be).double().cpu().numpy()
+    exact = va @ vb.T
+    assert (y[3] == 0).all() and (y[:, 3] == 0).all()
+    assert (np.abs(y - exact) <= bound(va, vb, exact, fmts, False)).all()
+
+
+@pytest.mark.parametrize("shape", [(1, 37, 128), (33, 70, 160), (200, 301, 256), (260, 514, 384)])
+def test_nothing_outside_is_written(lpq, shape):
+    M, N, K = shape
+    (a, ae, _), (b, be, _) = operand(M, K, R.FP8, 6), operand(N, K, R.FP4, 7)
+    buf = torch.full((M * N + 512,), 5.0, dtype=torch.bfloat16, device=DEV)
+    lpq.lpq_mx_matmul(a, ae, b, be, y=buf)
+    assert (buf[M * N:] == 5.0).all()
+    assert torch.equal(buf[:M * N].view(M, N), lpq.lpq_mx_matmul(a, ae, b, be))

@@ -165,3 +165,55 @@ def test_rmsnorm_binding(lib, recorder):
         with pytest.raises(exc):
             call()
     assert [c for c in recorder.calls if c != "lpq_rmsnorm_backward_workspace"] == []
+
+
+def test_matmul_validation(lib):
+    L = lib.raw()
+    Q = [P + (i << 24) for i in range(6)]
+    ok = dict(a=Q[0], ae=Q[1], fa=0, b=Q[2], be=Q[3], fb=1, M=4, N=16, K=64, y=Q[4], type=0, stream=None)
+
+    def call(**change):
+        return L.lpq_mx_matmul(*{**ok, **change}.values())
+
+    for k in ("a", "ae", "b", "be", "y"):
+        assert call(**{k: None}) == 1, k
+    for k, v in (("M", 0), ("N", -1), ("K", 0), ("K", 48), ("M", 1 << 31), ("N", 1 << 31), ("K", 1 << 31)):
+        assert call(**{k: v}) == 2, (k, v)
+    assert call(M=1 << 21, N=1 << 21) == 2 and call(M=1 << 21, K=1 << 21) == 2 and call(N=1 << 21, K=1 << 21) == 2
+    for k, v in (("fa", 2), ("fb", -1), ("type", 2), ("type", -1)):
+        assert call(**{k: v}) == 6, (k, v)
+    assert call(type=1) == 6 and call(type=1, fa=1, fb=0) == 6      # FP32 with an E4M3 operand
+    for k in ("a", "b", "y"):
+        assert call(**{k: ok[k] + 8}) == 3, k
+    assert call(y=Q[0] + 16) == 6 and call(y=Q[3]) == 6 and call(y=Q[2]) == 6
+    assert L.lpq_last_hip_error() == 0
+
+
+def test_matmul_binding(lib, recorder):
+    u8 = lambda *s: fake(torch.zeros(s, dtype=torch.uint8))
+    f8 = lambda *s: fake(torch.zeros(s, dtype=torch.uint8).view(torch.float8_e4m3fn))
+    a, ae, b, be = f8(4, 64), u8(4, 2), u8(16, 32), u8(16, 2)
+    bf = lambda *s: fake(torch.zeros(s, dtype=torch.bfloat16))
+    for exc, call in [
+            (TypeError, lambda: lib.lpq_mx_matmul(bf(4, 64), ae, b, be)),
+            (TypeError, lambda: lib.lpq_mx_matmul(fake(torch.zeros(4, 64, dtype=torch.int8)), ae, b, be)),
+            (ValueError, lambda: lib.lpq_mx_matmul(a, u8(4, 1), b, be)),
+            (ValueError, lambda: lib.lpq_mx_matmul(a, ae, b, u8(15, 2))),
+            (ValueError, lambda: lib.lpq_mx_matmul(a, ae, u8(16, 16), u8(16, 2))),          # another K
+            (ValueError, lambda: lib.lpq_mx_matmul(a, ae, b, be, b_format="nvfp4")),
+            (ValueError, lambda: lib.lpq_mx_matmul(a, ae, b, be, b_format="mxfp8")),         # then K differs
+            (TypeError, lambda: lib.lpq_mx_matmul(a, ae, b, be, out_dtype=torch.float16)),
+            (TypeError, lambda: lib.lpq_mx_matmul(a, ae, b, be, y=fake(torch.zeros(4, 16)))),
+            (ValueError, lambda: lib.lpq_mx_matmul(a, ae, b, be, y=bf(4, 15))),
+            (ValueError, lambda: lib.lpq_mx_matmul(f8(64, 4).t(), ae, b, be))]:
+        with pytest.raises(exc):
+            call()
+    assert recorder.calls == []
+
+
+def test_matmul_constants(lib):
+    import re
+    from tests.test_abi import HEADER
+    defs = {k: int(v) for k, v in re.findall(r"#define (LPQ_\w+) (\d+)", open(HEADER).read())}
+    assert {k: defs["LPQ_" + k.upper()] for k in lib.MX_FORMATS} == lib.MX_FORMATS
+    assert lib._MX_OUT == {torch.bfloat16: defs["LPQ_BF16"], torch.float32: defs["LPQ_F32"]}
