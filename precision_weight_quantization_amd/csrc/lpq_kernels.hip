@@ -670,6 +670,19 @@ lpq_status mx_matmul(const MatmulArgs& A, hipStream_t s) {
         hipLaunchKernelGGL((k_mx_matmul_rows<FP4B, FP4A, MT>), dim3((unsigned)grid), dim3(64 * kRowsWaves), 0, s, A, tiles_n);
         return launched();
     };
+    auto tile = [&](auto tn, auto tm, auto wn, auto wm) {
+        constexpr int TN = decltype(tn)::value, TM = decltype(tm)::value, WN = decltype(wn)::value, WM = decltype(wm)::value;
+        const int64_t nt = ((int64_t)A.N + TN - 1) / TN, mt = ((int64_t)A.M + TM - 1) / TM;
+        if (nt * mt > kMaxGridX) return LPQ_ERR_SHAPE;
+        hipLaunchKernelGGL((k_mx_matmul_tile<FP4B, FP4A, TN, TM, WN, WM>), dim3((unsigned)(nt * mt)), dim3(64 * WN * WM), 0, s, A,
+                           (int)nt, (int)mt);
+        return launched();
+    };
+    using std::integral_constant;
+    if (A.M > 64 && A.K <= (1 << 22)) {
+        if (A.M > 512) return tile(integral_constant<int, 256>{}, integral_constant<int, 256>{}, integral_constant<int, 2>{}, integral_constant<int, 4>{});
+        return tile(integral_constant<int, 128>{}, integral_constant<int, 128>{}, integral_constant<int, 2>{}, integral_constant<int, 2>{});
+    }
     if (A.M <= 16) return rows(std::integral_constant<int, 1>{});
     if (A.M <= 32) return rows(std::integral_constant<int, 2>{});
     return rows(std::integral_constant<int, 4>{});
