@@ -139,8 +139,8 @@ def _check(status: int, where: str) -> None:
 
 
 def _stream(stream) -> int:
-    if stream is None:
-        stream = torch.cuda.current_stream()
+    if stream is None:   # the current stream's handle, without a Stream object around it
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -149,10 +149,12 @@ def _launch(fn, where: str, like, stream, *args) -> None:
     stream or that device's current one."""
     index = like.device.index
     if index == torch.cuda.current_device():
-        _check(fn(*args, _stream(stream)), where)
+        status = fn(*args, _stream(stream))
     else:
         with torch.cuda.device(index):
-            _check(fn(*args, _stream(stream)), where)
+            status = fn(*args, _stream(stream))
+    if status != LPQ_OK:
+        raise LpqError(status, where)
 
 
 _HERE = contextlib.nullcontext()

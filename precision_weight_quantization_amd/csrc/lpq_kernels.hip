@@ -674,13 +674,14 @@ lpq_status mx_matmul(const MatmulArgs& A, hipStream_t s) {
         constexpr int TN = decltype(tn)::value, TM = decltype(tm)::value, WN = decltype(wn)::value, WM = decltype(wm)::value;
         const int64_t nt = ((int64_t)A.N + TN - 1) / TN, mt = ((int64_t)A.M + TM - 1) / TM;
         if (nt * mt > kMaxGridX) return LPQ_ERR_SHAPE;
-        hipLaunchKernelGGL((k_mx_matmul_tile<FP4B, FP4A, TN, TM, WN, WM>), dim3((unsigned)(nt * mt)), dim3(64 * WN * WM), 0, s, A,
-                           (int)nt, (int)mt);
+        const int64_t most = kComputeUnits * (TN == 256 ? 1 : 2);   // as many as run at one time: they go on from tile to tile
+        hipLaunchKernelGGL((k_mx_matmul_tile<FP4B, FP4A, TN, TM, WN, WM>), dim3((unsigned)(nt * mt < most ? nt * mt : most)),
+                           dim3(64 * WN * WM), 0, s, A, (int)nt, (int)mt);
         return launched();
     };
     using std::integral_constant;
-    if (A.M > 64 && A.K <= (1 << 22)) {
-        if (A.M > 512) return tile(integral_constant<int, 256>{}, integral_constant<int, 256>{}, integral_constant<int, 2>{}, integral_constant<int, 4>{});
+    if (A.M >= 128 && A.N >= 128 && A.K > 128 * stage_steps<FP4B, FP4A>() && A.K <= (1 << 22)) {
+        if (A.M > 512 && A.N >= 256) return tile(integral_constant<int, 256>{}, integral_constant<int, 256>{}, integral_constant<int, 2>{}, integral_constant<int, 4>{});
         return tile(integral_constant<int, 128>{}, integral_constant<int, 128>{}, integral_constant<int, 2>{}, integral_constant<int, 2>{});
     }
     if (A.M <= 16) return rows(std::integral_constant<int, 1>{});
