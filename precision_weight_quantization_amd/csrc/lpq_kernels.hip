@@ -680,7 +680,7 @@ lpq_status mx_matmul(const MatmulArgs& A, hipStream_t s) {
         return launched();
     };
     using std::integral_constant;
-    if (A.M >= 128 && A.N >= 128 && A.K > 128 * stage_steps<FP4B, FP4A>() && A.K <= (1 << 22)) {
+    if (A.M >= 128 && A.N >= 128 && A.K > 128 * stage_steps<FP4B, FP4A>() && A.K <= (1 << 22) && A.N <= (1 << 22)) {
         if (A.M > 512 && A.N >= 256) return tile(integral_constant<int, 256>{}, integral_constant<int, 256>{}, integral_constant<int, 2>{}, integral_constant<int, 4>{});
         return tile(integral_constant<int, 128>{}, integral_constant<int, 128>{}, integral_constant<int, 2>{}, integral_constant<int, 2>{});
     }

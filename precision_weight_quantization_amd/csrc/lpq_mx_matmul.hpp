@@ -166,16 +166,11 @@ struct Stage {
 // goes into m0, and one wait state lies between the two).  The
 // compiler does not see these loads: it would wait for all of them before any
 // read of LDS, the other stage's included.  They write no register, so nothing
-// else depends on them.  lds_arrived<N>() waits for all but the wave's N newest
-// memory operations.
+// else depends on them.  lds_arrived() waits for the wave's own.
 __device__ __forceinline__ void load_to_lds(const uint8_t* base, uint32_t offset, uint32_t to) {
     __asm__ volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"{m0}"(to), "v"(offset), "s"(base) : "memory");
 }
-template <int N>
-__device__ __forceinline__ void lds_arrived() {
-    static_assert(N < 64, "the counter's range");
-    __asm__ volatile("s_waitcnt vmcnt(%0)" ::"i"(N) : "memory");
-}
+__device__ __forceinline__ void lds_arrived() { __asm__ volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 
 // The order of tiles.  Workgroups go to the 8 XCDs in turn, and each XCD has an
 // L2 of its own: XCD x takes a run of tiles of its own, in columns of kTileGroup
@@ -363,13 +358,16 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void k_mx_matmul_tile(MatmulArgs A
             for (int j = 0; j < FM; j++) __asm__ volatile("" : "+v"(c[i][j]));
     };
     Frag<FP4A> fa[FM];
-    Frag<FP4B> fb;
+    // Rows of b are read kAhead rows before their products: an E2M1 row's products take half as
+    // long as an E4M3 row's, and the read no less.
+    constexpr int kAhead = FP4B && FP4A ? 2 : 1;
+    Frag<FP4B> fb[kAhead];
     // a row of products; then(j) may load what takes the place of fa[j] from there on
     auto products = [&](int i, auto then) {
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int j = 0; j < FM; j++) {
-            c[i][j] = mfma<FP4B, FP4A>(fb, fa[j], c[i][j]);
+            c[i][j] = mfma<FP4B, FP4A>(fb[0], fa[j], c[i][j]);
             then(j);
             __builtin_amdgcn_sched_barrier(0);
         }
@@ -378,28 +376,32 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void k_mx_matmul_tile(MatmulArgs A
     open_tile();
     load_stage(0);
     put_scales(0);
-    lds_arrived<0>();
+    lds_arrived();
     __syncthreads();
     load_stage(1);
     scales_of(0);
 #pragma unroll
     for (int j = 0; j < FM; j++) fa[j] = frag_a(j, 0);
-    fb = frag_b(0, 0);
+    auto first_rows = [&]() {
+#pragma unroll
+        for (int i = 0; i < kAhead; i++) fb[i] = frag_b(i, 0);
+    };
+    first_rows();
 
-    constexpr int kStores = FM * FN / 4 * 2;   // of a wave, for a tile stored by way of LDS
-    const bool by_lds = A.N % 8 == 0 && !A.f32;
-    bool stored = false;   // kStores stores are newer than the loads of the next stage
     int buf = 0;
     for (int tile = first_tile; tile < run_end; tile += slots) {
         clear();
         for (int s = 0; s < steps; s++) {
 #pragma unroll
             for (int i = 0; i < FN * KS - 1; i++) {
-                const Frag<FP4B> next = frag_b((i + 1) % FN, (i + 1) / FN);
+                Frag<FP4B> next;
+                if (i + kAhead < FN * KS) next = frag_b((i + kAhead) % FN, (i + kAhead) / FN);
                 products(i % FN, [&](int j) {
                     if (i % FN == FN - 1) fa[j] = frag_a(j, i / FN + 1);
                 });
-                fb = next;
+#pragma unroll
+                for (int x = 0; x + 1 < kAhead; x++) fb[x] = fb[x + 1];
+                fb[kAhead - 1] = next;
             }
             // The stage's one barrier, where a wave has read all it needs of the stage but
             // still has a row of products to do: what follows (the loads of the stage after
@@ -408,9 +410,7 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void k_mx_matmul_tile(MatmulArgs A
             pin();
             const int next_step = s + 1 == steps ? 0 : s + 1;
             if (next_step % kGroup == 0) put_scales(parity ^ 1);
-            if (stored) lds_arrived<kStores>();
-            else lds_arrived<0>();
-            stored = false;
+            lds_arrived();
             if (next_step == full) zero_tail(next_step, buf ^ 1);
             __syncthreads();
             if (load_tile < run_end) load_stage(buf);   // of this tile or of the next
@@ -418,48 +418,69 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void k_mx_matmul_tile(MatmulArgs A
             parity ^= next_step % kGroup == 0;
             b0 ^= kNextCodes, b1 ^= kNextCodes, a0 ^= kNextCodes, a1 ^= kNextCodes;
             scales_of(next_step);
-            const Frag<FP4B> next = frag_b(0, 0);
+            Frag<FP4B> next[kAhead];
+#pragma unroll
+            for (int i = 0; i < kAhead; i++) next[i] = frag_b(i, 0);
             products(FN - 1, [&](int j) { fa[j] = frag_a(j, 0); });
-            fb = next;
+#pragma unroll
+            for (int i = 0; i < kAhead; i++) fb[i] = next[i];
             pin();
         }
         int64_t n0, m0;
         origin(tile, n0, m0);
         n0 += wn * FN * 16, m0 += wm * FM * 16;
-        if (!by_lds) {
+        int N = A.N;   // opaque here: else the offsets of every store are formed before the first tile and kept
+        __asm__ volatile("" : "+s"(N));
+        // Rows by way of LDS, 16 rows of 128 bytes at a time, so that 128 bytes of a row leave
+        // in one piece: stored from the accumulators each instruction would write 32 bytes of
+        // 16 rows (measured: 17 us of 233 at 8192 x 9728 x 2560).  Swizzled as a stage's rows
+        // are.  Non-temporal: 9 us of 207 there.
+        auto store_rows = [&](auto f32) {
+            constexpr bool F32 = decltype(f32)::value;
+            constexpr int kSize = F32 ? 4 : 2, kFrags = F32 ? 2 : 4;   // 16-column results in 128 bytes
+            uint8_t* mine = lds + kOut + wave * 2048;
+            uint8_t* y = static_cast<uint8_t*>(A.y) + (m0 * N + n0) * kSize;   // uniform
+            const uint32_t off = (uint32_t)(lane >> 3) * N * kSize + (lane & 7) * 16;
+#pragma unroll
+            for (int j = 0; j < FM; j++) {
+#pragma unroll
+                for (int h = 0; h < FN; h += kFrags) {
+#pragma unroll
+                    for (int i = 0; i < kFrags; i++) {
+                        const v4f v = c[h + i][j];
+                        if constexpr (F32)
+                            *reinterpret_cast<v4f*>(mine + r * 128 + ((i * 4 + g) ^ ((r >> 1) & 7)) * 16) = v;
+                        else
+                            *reinterpret_cast<v2u*>(mine + r * 128 + ((i * 2 + (g >> 1)) ^ ((r >> 1) & 7)) * 16 + (g & 1) * 8) =
+                                v2u{bf16x2(v[0], v[1]), bf16x2(v[2], v[3])};
+                    }
+                    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll
+                    for (int x = 0; x < 16; x += 8) {
+                        const int row = x + (lane >> 3);
+                        const v4u v = *reinterpret_cast<const v4u*>(mine + row * 128 + ((lane & 7) ^ ((row >> 1) & 7)) * 16);
+                        store<true>(reinterpret_cast<v4u*>(y + ((int64_t)(j * 16 + x) * N + h * 16) * kSize + off), v);
+                    }
+                    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+                }
+            }
+        };
+        if (A.f32 ? N % 4 == 0 : N % 8 == 0) {
+            if (A.f32) store_rows(std::true_type{});
+            else store_rows(std::false_type{});
+        } else {
+            uint8_t* y = static_cast<uint8_t*>(A.y) + (m0 * N + n0) * (A.f32 ? 4 : 2);
 #pragma unroll
             for (int j = 0; j < FM; j++)
 #pragma unroll
-                for (int i = 0; i < FN; i++) store_y4(A, m0 + j * 16 + r, (int)n0 + i * 16 + g * 4, c[i][j]);
-            continue;
+                for (int i = 0; i < FN; i++)
+#pragma unroll
+                    for (int x = 0; x < 4; x++) {
+                        const uint32_t at = (uint32_t)(j * 16 + r) * N + i * 16 + g * 4 + x;
+                        if (A.f32) store<false>(reinterpret_cast<float*>(y) + at, c[i][j][x]);
+                        else store<false>(reinterpret_cast<uint16_t*>(y) + at, (uint16_t)bf16x2(c[i][j][x], 0.0f));
+                    }
         }
-        // BF16 rows by way of LDS, 16 rows of 64 columns at a time, so that 128 bytes of a row
-        // leave in one piece: stored from the accumulators each instruction would write 32
-        // bytes of 16 rows (measured: 17 us of 233 at 8192 x 9728 x 2560).  Swizzled as a
-        // stage's rows are.
-        uint8_t* mine = lds + kOut + wave * 2048;
-        uint16_t* y = static_cast<uint16_t*>(A.y);
-#pragma unroll
-        for (int j = 0; j < FM; j++) {
-#pragma unroll
-            for (int h = 0; h < FN; h += 4) {
-#pragma unroll
-                for (int i = 0; i < 4; i++) {
-                    const v4f v = c[h + i][j];
-                    *reinterpret_cast<v2u*>(mine + r * 128 + ((i * 2 + (g >> 1)) ^ ((r >> 1) & 7)) * 16 + (g & 1) * 8) =
-                        v2u{bf16x2(v[0], v[1]), bf16x2(v[2], v[3])};
-                }
-                __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-#pragma unroll
-                for (int x = 0; x < 16; x += 8) {
-                    const int row = x + (lane >> 3), piece = lane & 7;
-                    const v4u v = *reinterpret_cast<const v4u*>(mine + row * 128 + (piece ^ ((row >> 1) & 7)) * 16);
-                    store<false>(reinterpret_cast<v4u*>(y + (m0 + j * 16 + row) * A.N + n0 + h * 16 + piece * 8), v);
-                }
-                __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-            }
-        }
-        stored = true;
     }
 }
 
