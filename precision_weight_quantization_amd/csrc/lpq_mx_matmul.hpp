@@ -162,13 +162,15 @@ struct Stage {
     static constexpr int kElems = FP4 ? 32 : 16;   // elements of a 16-byte piece
 };
 
-// 16 bytes of each lane from memory to LDS: lane l's to byte `to` + 16 * l (`to`
-// goes into m0, and one wait state lies between the two).  The
-// compiler does not see these loads: it would wait for all of them before any
-// read of LDS, the other stage's included.  They write no register, so nothing
+// 16 bytes of each lane from memory to LDS: lane l's to byte `to` + 16 * l.  The
+// 5 wait states are what a vector memory instruction needs behind a vector
+// instruction that wrote its scalar base (1 behind the write of m0); the
+// compiler does not look into the block to add them.  Nor does it see the load:
+// it would wait for all of them before any read of LDS, the other stage's
+// included.  They write no register, so nothing
 // else depends on them.  lds_arrived() waits for the wave's own.
 __device__ __forceinline__ void load_to_lds(const uint8_t* base, uint32_t offset, uint32_t to) {
-    __asm__ volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"{m0}"(to), "v"(offset), "s"(base) : "memory");
+    __asm__ volatile("s_nop 4\n\tglobal_load_lds_dwordx4 %1, %2" ::"{m0}"(to), "v"(offset), "s"(uniform_ptr(base)) : "memory");
 }
 __device__ __forceinline__ void lds_arrived() { __asm__ volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 
@@ -187,6 +189,15 @@ __device__ __forceinline__ void tile_at(int t, int tiles_n, int tiles_m, int& n,
 template <bool FP4B, bool FP4A>
 constexpr int stage_steps() {
     return FP4B && FP4A ? 2 : 1;
+}
+
+// f(integral_constant<int, 0>), f(integral_constant<int, 1>), ... up to N - 1.
+template <int N, typename F>
+__device__ __forceinline__ void static_for(F&& f) {
+    if constexpr (N > 0) {
+        static_for<N - 1>(f);
+        f(std::integral_constant<int, N - 1>{});
+    }
 }
 
 // N >= TN, M >= TM, at least two stages.
@@ -273,9 +284,26 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void k_mx_matmul_tile(MatmulArgs A
             }
         }
     };
+    // In LDS the bytes of 4 rows that are 16 apart lie side by side (the 64 rows of a wave's
+    // load: 16 dwords for each of the 16 blocks), so that a lane reads the scales of 4 of its
+    // 16-row pieces at once and each product picks its byte: a byte read for every piece took
+    // 10 of 143 us (MXFP4, 8192 x 9728 x 2560).  Lane (i, r) = (lane / 16, lane % 16) holds the
+    // 16 bytes of row 16 i + r: a transpose of 4 x 4 dwords over i, then of 4 x 4 bytes in place.
     auto put_scales = [&](int parity) {
 #pragma unroll
-        for (int i = 0; i < SR; i++) *reinterpret_cast<v4u*>(lds + kScales0 + parity * kScales + (i * T + tid) * 16) = sc[i];
+        for (int i = 0; i < SR; i++) {
+            const auto p02 = __builtin_amdgcn_permlane32_swap(sc[i][0], sc[i][2], false, false);
+            const auto p13 = __builtin_amdgcn_permlane32_swap(sc[i][1], sc[i][3], false, false);
+            const auto p01 = __builtin_amdgcn_permlane16_swap(p02[0], p13[0], false, false);
+            const auto p23 = __builtin_amdgcn_permlane16_swap(p02[1], p13[1], false, false);
+            uint32_t* at = reinterpret_cast<uint32_t*>(lds + kScales0 + parity * kScales + (i * T + wave * 64) * 16) + g * 64 + r;
+#pragma unroll
+            for (int b = 0; b < 4; b++) {
+                const uint32_t pick = b | (4 + b) << 8;
+                const uint32_t lo = __builtin_amdgcn_perm(p01[1], p01[0], pick), hi = __builtin_amdgcn_perm(p23[1], p23[0], pick);
+                at[b * 16] = __builtin_amdgcn_perm(hi, lo, 0x05040100u);
+            }
+        }
     };
     auto last_piece = [&](int step, int elems) { return min(A.K - step * BK, BK) / elems - 1; };
     // the next stage of the tile being loaded, into buffer `buf`, and its scale group if it opens one
@@ -317,27 +345,37 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void k_mx_matmul_tile(MatmulArgs A
     uint32_t sb[KS], sa[KS];
     int parity = 0;   // of the current scale group
     auto scales_of = [&](int step) {   // blocks past K take the byte of the last one (their codes are zeros)
-        const int at = step * 4 * KS, last = blocks - 1 - at;
-        const uint32_t to = kScales0 + parity * kScales + at - group_start(step / kGroup);
+        const int at = step * 4 * KS, start = group_start(step / kGroup), last = blocks - 1 - start;
+        const uint32_t to = kScales0 + parity * kScales + r * 4;
 #pragma unroll
         for (int x = 0; x < KS; x++) {
-            const int y = min(x * 4 + g, last);
-            sb[x] = to + row_b * 16 + y;
-            sa[x] = to + (TN + row_a) * 16 + y;
+            const int y = min(at - start + x * 4 + g, last);
+            sb[x] = to + wn * FN * 256 + y * 64;
+            sa[x] = to + TN * 16 + wm * FM * 256 + y * 64;
         }
+    };
+    constexpr int SB = FN / 4, SA = (FM + 3) / 4;
+    struct Scales {
+        uint32_t b[SB], a[SA];
+    };
+    auto read_scales = [&](int ks) {
+        Scales v;
+#pragma unroll
+        for (int i = 0; i < SB; i++) v.b[i] = *reinterpret_cast<const uint32_t*>(lds + sb[ks] + i * 1024);
+#pragma unroll
+        for (int j = 0; j < SA; j++) v.a[j] = *reinterpret_cast<const uint32_t*>(lds + sa[ks] + j * 1024);
+        return v;
     };
     auto frag_b = [&](int i, int ks) {
         Frag<FP4B> f;
         f.lo = *reinterpret_cast<const v4u*>(lds + (ks ? b1 : b0) + i * 16 * PB);
         if constexpr (!FP4B) f.hi = *reinterpret_cast<const v4u*>(lds + b1 + i * 16 * PB);
-        f.scale = lds[sb[ks] + i * 256];
         return f;
     };
     auto frag_a = [&](int i, int ks) {
         Frag<FP4A> f;
         f.lo = *reinterpret_cast<const v4u*>(lds + (ks ? a1 : a0) + i * 16 * PA);
         if constexpr (!FP4A) f.hi = *reinterpret_cast<const v4u*>(lds + a1 + i * 16 * PA);
-        f.scale = lds[sa[ks] + i * 256];
         return f;
     };
 
@@ -362,15 +400,18 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void k_mx_matmul_tile(MatmulArgs A
     // long as an E4M3 row's, and the read no less.
     constexpr int kAhead = FP4B && FP4A ? 2 : 1;
     Frag<FP4B> fb[kAhead];
+    Scales sv;
     // a row of products; then(j) may load what takes the place of fa[j] from there on
-    auto products = [&](int i, auto then) {
+    auto products = [&](auto row, auto then) {
+        constexpr int i = decltype(row)::value;
         __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-        for (int j = 0; j < FM; j++) {
-            c[i][j] = mfma<FP4B, FP4A>(fb[0], fa[j], c[i][j]);
+        static_for<FM>([&](auto col) {
+            constexpr int j = decltype(col)::value;
+            c[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(frag_regs(fb[0]), frag_regs(fa[j]), c[i][j], FP4B ? 4 : 0,
+                                                                       FP4A ? 4 : 0, i % 4, (int)sv.b[i / 4], j % 4, (int)sv.a[j / 4]);
             then(j);
             __builtin_amdgcn_sched_barrier(0);
-        }
+        });
     };
 
     open_tile();
@@ -387,22 +428,27 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void k_mx_matmul_tile(MatmulArgs A
         for (int i = 0; i < kAhead; i++) fb[i] = frag_b(i, 0);
     };
     first_rows();
+    sv = read_scales(0);
 
     int buf = 0;
     for (int tile = first_tile; tile < run_end; tile += slots) {
         clear();
         for (int s = 0; s < steps; s++) {
+            static_for<FN * KS - 1>([&](auto at) {
+                constexpr int x = decltype(at)::value, i = x % FN, ks = x / FN;
+                Frag<FP4B> next = fb[kAhead - 1];
+                if constexpr (x + kAhead < FN * KS) next = frag_b((x + kAhead) % FN, (x + kAhead) / FN);
+                if constexpr (i == FN - 1) {   // of the stage's first step, with the reads of its second
+                    const Scales next_sv = read_scales(ks + 1);
+                    products(std::integral_constant<int, i>{}, [&](int j) { fa[j] = frag_a(j, ks + 1); });
+                    sv = next_sv;
+                } else {
+                    products(std::integral_constant<int, i>{}, [](int) {});
+                }
 #pragma unroll
-            for (int i = 0; i < FN * KS - 1; i++) {
-                Frag<FP4B> next;
-                if (i + kAhead < FN * KS) next = frag_b((i + kAhead) % FN, (i + kAhead) / FN);
-                products(i % FN, [&](int j) {
-                    if (i % FN == FN - 1) fa[j] = frag_a(j, i / FN + 1);
-                });
-#pragma unroll
-                for (int x = 0; x + 1 < kAhead; x++) fb[x] = fb[x + 1];
+                for (int k = 0; k + 1 < kAhead; k++) fb[k] = fb[k + 1];
                 fb[kAhead - 1] = next;
-            }
+            });
             // The stage's one barrier, where a wave has read all it needs of the stage but
             // still has a row of products to do: what follows (the loads of the stage after
             // the next into the LDS just freed, the first reads of the next) goes on beside
@@ -421,7 +467,9 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void k_mx_matmul_tile(MatmulArgs A
             Frag<FP4B> next[kAhead];
 #pragma unroll
             for (int i = 0; i < kAhead; i++) next[i] = frag_b(i, 0);
-            products(FN - 1, [&](int j) { fa[j] = frag_a(j, 0); });
+            const Scales next_sv = read_scales(0);
+            products(std::integral_constant<int, FN - 1>{}, [&](int j) { fa[j] = frag_a(j, 0); });
+            sv = next_sv;
 #pragma unroll
             for (int i = 0; i < kAhead; i++) fb[i] = next[i];
             pin();
