@@ -149,7 +149,7 @@ def _launch(fn, where: str, like, stream, *args) -> None:
     stream or that device's current one."""
     index = like.device.index
     if index == torch.cuda.current_device():
-        status = fn(*args, _stream(stream))
+        status = fn(*args, torch._C._cuda_getCurrentRawStream(index) if stream is None else _stream(stream))
     else:
         with torch.cuda.device(index):
             status = fn(*args, _stream(stream))

@@ -9,6 +9,7 @@ namespace {
 
 constexpr int kThreads = LPQ_FLAT_THREADS;   // flat kernels
 constexpr int kTile = 128;
+constexpr int kComputeUnits = 256;       // CUs of the card
 constexpr bool kNTL = LPQ_NTL != 0;
 constexpr bool kNTS = LPQ_NTS != 0;
 constexpr int kMaxSeg = 8;               // segments per launch (longer lists are split)

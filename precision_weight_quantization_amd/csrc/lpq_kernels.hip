@@ -619,12 +619,15 @@ lpq_status rmsnorm(const NormArgs& A, void* stream) {
     });
 }
 
-// Workgroups of the backward pass: at most LPQ_NORMG_GROUPS, each with a
-// partial sum of dgamma.
+// Workgroups of the backward pass, each with a partial sum of dgamma that costs
+// 8 bytes a column: one per CU for long rows (8192 x 2560: 34 us with 256, 38
+// with 512, 44 with 1024), up to four for short ones, whose partial sums are
+// small and whose loads need more waves to wait beside (98301 x 128: 29, 18 and
+// 15 us).
 int64_t norm_grad_groups(int64_t M, int64_t N) {
     return by_row(N, [&](auto shape) {
         constexpr int G = decltype(shape)::g, kRows = norm_threads(G) / G;
-        const int64_t groups = (M + kRows - 1) / kRows, most = LPQ_NORMG_GROUPS;
+        const int64_t groups = (M + kRows - 1) / kRows, each = 1024 / N, most = kComputeUnits * (each < 1 ? 1 : each > 4 ? 4 : each);
         return groups < most ? groups : most;
     });
 }
@@ -664,10 +667,10 @@ template <bool FP4A, bool FP4B>
 lpq_status mx_matmul(const MatmulArgs& A, hipStream_t s) {
     const int tiles_n = (A.N + 15) / 16;
     auto rows = [&](auto mt) {
-        constexpr int MT = decltype(mt)::value;
+        constexpr int MT = decltype(mt)::value, U = MT == 1 ? LPQ_ROWS_U1 : MT == 2 ? LPQ_ROWS_U2 : LPQ_ROWS_U4;
         const int64_t grid = ((int64_t)A.M + 16 * MT - 1) / (16 * MT) * tiles_n;
         if (grid > kMaxGridX) return LPQ_ERR_SHAPE;
-        hipLaunchKernelGGL((k_mx_matmul_rows<FP4B, FP4A, MT>), dim3((unsigned)grid), dim3(64 * kRowsWaves), 0, s, A, tiles_n);
+        hipLaunchKernelGGL((k_mx_matmul_rows<FP4B, FP4A, MT, U>), dim3((unsigned)grid), dim3(64 * kRowsWaves), 0, s, A, tiles_n);
         return launched();
     };
     auto tile = [&](auto tn, auto tm, auto wn, auto wm) {

@@ -96,7 +96,9 @@ __device__ __forceinline__ void store_y4(const MatmulArgs& A, int64_t m, int n, 
 // operands go from memory to registers; each weight is read once.
 constexpr int kRowsWaves = 4;
 
-template <bool FP4B, bool FP4A, int MT>
+// U steps' loads go out together: a wave has few steps, and each round trip to
+// memory costs as much as all of them.
+template <bool FP4B, bool FP4A, int MT, int U>
 __global__ __launch_bounds__(64 * kRowsWaves) void k_mx_matmul_rows(MatmulArgs A, int tiles_n) {
     __shared__ v4f part[kRowsWaves][MT][64];
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, g = lane >> 4, r = lane & 15;
@@ -117,10 +119,20 @@ __global__ __launch_bounds__(64 * kRowsWaves) void k_mx_matmul_rows(MatmulArgs A
         ae[i] = A.ae + (in_m[i] ? m : 0) * (A.K / 32);
         c[i] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
     }
-    for (int k0 = wave * 128; k0 < A.K; k0 += kRowsWaves * 128) {
-        const Frag<FP4B> fb = load_frag<FP4B>(b, be, in_n, k0, A.K, g);
+    for (int k = wave * 128; k < A.K; k += kRowsWaves * 128 * U) {
+        Frag<FP4B> fb[U];
+        Frag<FP4A> fa[U][MT];
 #pragma unroll
-        for (int i = 0; i < MT; i++) c[i] = mfma<FP4B, FP4A>(fb, load_frag<FP4A>(a[i], ae[i], in_m[i], k0, A.K, g), c[i]);
+        for (int u = 0; u < U; u++) {
+            const int k0 = k + u * kRowsWaves * 128;
+            fb[u] = load_frag<FP4B>(b, be, in_n, k0, A.K, g);
+#pragma unroll
+            for (int i = 0; i < MT; i++) fa[u][i] = load_frag<FP4A>(a[i], ae[i], in_m[i], k0, A.K, g);
+        }
+#pragma unroll
+        for (int u = 0; u < U; u++)
+#pragma unroll
+            for (int i = 0; i < MT; i++) c[i] = mfma<FP4B, FP4A>(fb[u], fa[u][i], c[i]);
     }
 #pragma unroll
     for (int i = 0; i < MT; i++) part[wave][i][lane] = c[i];
@@ -178,7 +190,7 @@ __device__ __forceinline__ void lds_arrived() { __asm__ volatile("s_waitcnt vmcn
 // L2 of its own: XCD x takes a run of tiles of its own, in columns of kTileGroup
 // rows of tiles, so that the workgroups that run on it at one time share few
 // rows of either operand.
-constexpr int kXcds = 8, kTileGroup = 8, kComputeUnits = 256;
+constexpr int kXcds = 8, kTileGroup = 8;
 __device__ __forceinline__ void tile_at(int t, int tiles_n, int tiles_m, int& n, int& m) {
     const int first = t / (kTileGroup * tiles_n) * kTileGroup;
     const int rows = min(tiles_m - first, kTileGroup), in = t - first * tiles_n;

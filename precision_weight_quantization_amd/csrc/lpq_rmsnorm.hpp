@@ -76,6 +76,13 @@ __global__ __launch_bounds__(norm_threads(G)) void k_rmsnorm(NormArgs A) {
         const bool in = in_row && c < A.N;
         h[u] = in ? load<kNTL>(reinterpret_cast<const v4u*>(A.x + at + c)) : v4u{};
     }
+    // gamma's loads go out with the row's: a wave of few rows would wait for them after the sum
+    v4u gm[U];
+#pragma unroll
+    for (int u = 0; u < U; u++) {
+        const int c = (u * G + t) * 8;
+        gm[u] = c < A.N ? load<false>(reinterpret_cast<const v4u*>(A.gamma + c)) : v4u{};
+    }
     if (A.residual) {
         v4u r[U];
 #pragma unroll
@@ -105,8 +112,7 @@ __global__ __launch_bounds__(norm_threads(G)) void k_rmsnorm(NormArgs A) {
     for (int u = 0; u < U; u++) {
         const int c = (u * G + t) * 8;
         const bool in = in_row && c < A.N;
-        const v4u gm = c < A.N ? load<false>(reinterpret_cast<const v4u*>(A.gamma + c)) : v4u{};
-        const F8 f = widen8(h[u]), g = widen8(gm);
+        const F8 f = widen8(h[u]), g = widen8(gm[u]);
         v4u y;
 #pragma unroll
         for (int k = 0; k < 4; k++) y[k] = bf16x2(f.x[2 * k] * r * g.x[2 * k], f.x[2 * k + 1] * r * g.x[2 * k + 1]);
@@ -223,17 +229,20 @@ __global__ __launch_bounds__(norm_threads(G)) void k_rmsnorm_grad(NormGradArgs A
     }
 }
 
-// dgamma[c] (+)= the sum of P partials in a fixed order: 16 threads of a column
-// each take every 16th partial, then their sums are added in thread order.
-constexpr int kDgCols = 64, kDgSlices = 16;
+// dgamma[c] (+)= the sum of P partials in a fixed order: 32 threads of a column
+// each take every 32nd partial, 8 loads at a time, then their sums are added in
+// thread order.
+constexpr int kDgCols = 32, kDgSlices = 32;
 __global__ __launch_bounds__(kDgCols* kDgSlices) void k_rmsnorm_dgamma(const float* part, int32_t P, int32_t N, int accumulate,
                                                                       float* dgamma) {
     __shared__ float sum[kDgSlices][kDgCols];
     const int x = threadIdx.x % kDgCols, s = threadIdx.x / kDgCols;
     const int c = blockIdx.x * kDgCols + x;
     float a = 0.0f;
-    if (c < N)
+    if (c < N) {
+#pragma unroll 8
         for (int p = s; p < P; p += kDgSlices) a += part[(int64_t)p * N + c];
+    }
     sum[s][x] = a;
     __syncthreads();
     if (s == 0 && c < N) {
