@@ -663,33 +663,60 @@ lpq_status rmsnorm_grad(NormGradArgs A, float* dgamma, int accumulate, void* wor
     return launched();
 }
 
+template <int N>
+using Int = std::integral_constant<int, N>;
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// Which kernel a product takes.
+//  * Tiles of 128 x 128 or more by way of LDS, from 64 such tiles on: fewer leave
+//    most of the card idle, and a stage's way from memory to LDS takes as long for
+//    one tile as for 256 (measured, MXFP8 x MXFP4 at k = 2560: 128 x 2560 15 us as
+//    20 tiles and 10 by rows; 128 x 9728 18 us as 76 tiles and 36 by rows).
+//  * Among the tiles the shape that takes the least time for its rounds of the
+//    card.  One round (256 tiles, one on each CU) of 256 x 256 counts 2; 256 x 192
+//    1.8; 128 x 128 0.95 alone, 1.1 with two on each CU, and 1.6 where many rounds
+//    keep memory busy, which larger tiles ask less of (measured at k = 2560, MXFP8:
+//    37 us, 33 us, 16 and 20 us, 28 us a round).
+//  * Rows otherwise, in workgroups of as many rows of b as leave 128 workgroups: each
+//    reads its rows of a once (64 x 9728 x 2560: 23 us with 16, 19 with 32 and 14
+//    with 64; 64 x 2560 x 2560, 40 workgroups with 64: 9 us with 16, 12 with 64).
 template <bool FP4A, bool FP4B>
 lpq_status mx_matmul(const MatmulArgs& A, hipStream_t s) {
-    const int tiles_n = (A.N + 15) / 16;
-    auto rows = [&](auto mt) {
-        constexpr int MT = decltype(mt)::value, U = MT == 1 ? LPQ_ROWS_U1 : MT == 2 ? LPQ_ROWS_U2 : LPQ_ROWS_U4;
-        const int64_t grid = ((int64_t)A.M + 16 * MT - 1) / (16 * MT) * tiles_n;
+    auto rows = [&](auto nt, auto mt, auto u) {
+        constexpr int NT = decltype(nt)::value, MT = decltype(mt)::value, U = decltype(u)::value;
+        const int64_t tiles_n = ceil_div(A.N, 16 * NT), grid = ceil_div(A.M, 16 * MT) * tiles_n;
         if (grid > kMaxGridX) return LPQ_ERR_SHAPE;
-        hipLaunchKernelGGL((k_mx_matmul_rows<FP4B, FP4A, MT, U>), dim3((unsigned)grid), dim3(64 * kRowsWaves), 0, s, A, tiles_n);
+        hipLaunchKernelGGL((k_mx_matmul_rows<FP4B, FP4A, NT, MT, U>), dim3((unsigned)grid), dim3(64 * kRowsWaves), 0, s, A, (int)tiles_n);
         return launched();
     };
     auto tile = [&](auto tn, auto tm, auto wn, auto wm) {
         constexpr int TN = decltype(tn)::value, TM = decltype(tm)::value, WN = decltype(wn)::value, WM = decltype(wm)::value;
-        const int64_t nt = ((int64_t)A.N + TN - 1) / TN, mt = ((int64_t)A.M + TM - 1) / TM;
+        const int64_t nt = ceil_div(A.N, TN), mt = ceil_div(A.M, TM);
         if (nt * mt > kMaxGridX) return LPQ_ERR_SHAPE;
         const int64_t most = kComputeUnits * (TN == 256 ? 1 : 2);   // as many as run at one time: they go on from tile to tile
         hipLaunchKernelGGL((k_mx_matmul_tile<FP4B, FP4A, TN, TM, WN, WM>), dim3((unsigned)(nt * mt < most ? nt * mt : most)),
                            dim3(64 * WN * WM), 0, s, A, (int)nt, (int)mt);
         return launched();
     };
-    using std::integral_constant;
-    if (A.M >= 128 && A.N >= 128 && A.K > 128 * stage_steps<FP4B, FP4A>() && A.K <= (1 << 22) && A.N <= (1 << 22)) {
-        if (A.M > 512 && A.N >= 256) return tile(integral_constant<int, 256>{}, integral_constant<int, 256>{}, integral_constant<int, 2>{}, integral_constant<int, 4>{});
-        return tile(integral_constant<int, 128>{}, integral_constant<int, 128>{}, integral_constant<int, 2>{}, integral_constant<int, 2>{});
+    const int64_t n128 = ceil_div(A.N, 128) * ceil_div(A.M, 128);
+    const bool limits = A.K > 128 * stage_steps<FP4B, FP4A>() && A.K <= (1 << 22) && A.N <= (1 << 22);
+    if (limits && A.M >= 128 && A.N >= 128 && n128 >= 64) {
+        const double none = 1e30;
+        const double c128 = n128 <= 256 ? 0.95 : ceil_div(n128, 512) * (n128 <= 2048 ? 1.1 : 1.6);
+        const double c256 = A.M >= 256 && A.N >= 256 ? 2.0 * ceil_div(ceil_div(A.N, 256) * ceil_div(A.M, 256), 256) : none;
+        if constexpr (!FP4A || FP4B) {   // an E2M1 a beside an E4M3 b has too few pieces for 192 rows
+            const double c192 = A.M >= 192 && A.N >= 256 ? 1.8 * ceil_div(ceil_div(A.N, 256) * ceil_div(A.M, 192), 256) : none;
+            if (c192 < c256 && c192 < c128) return tile(Int<256>{}, Int<192>{}, Int<2>{}, Int<4>{});
+        }
+        if (c256 < c128) return tile(Int<256>{}, Int<256>{}, Int<2>{}, Int<4>{});
+        return tile(Int<128>{}, Int<128>{}, Int<2>{}, Int<2>{});
     }
-    if (A.M <= 16) return rows(std::integral_constant<int, 1>{});
-    if (A.M <= 32) return rows(std::integral_constant<int, 2>{});
-    return rows(std::integral_constant<int, 4>{});
+    if (A.M <= 16) return rows(Int<1>{}, Int<1>{}, Int<3>{});
+    const int64_t mt = A.M <= 32 ? 1 : ceil_div(A.M, 64);
+    const int nt = mt * ceil_div(A.N, 64) >= 128 ? 4 : mt * ceil_div(A.N, 32) >= 128 ? 2 : 1;
+    if (A.M <= 32) return nt == 4 ? rows(Int<4>{}, Int<2>{}, Int<1>{}) : nt == 2 ? rows(Int<2>{}, Int<2>{}, Int<2>{}) : rows(Int<1>{}, Int<2>{}, Int<2>{});
+    return nt == 4 ? rows(Int<4>{}, Int<4>{}, Int<1>{}) : nt == 2 ? rows(Int<2>{}, Int<4>{}, Int<1>{}) : rows(Int<1>{}, Int<4>{}, Int<1>{});
 }
 
 // Host-side checks of an observer call; the workgroup count on success.

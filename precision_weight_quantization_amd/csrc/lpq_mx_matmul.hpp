@@ -91,59 +91,67 @@ __device__ __forceinline__ void store_y4(const MatmulArgs& A, int64_t m, int n, 
     }
 }
 
-// Few rows of a: a workgroup takes 16 rows of b and 16 * MT rows of a, its
+// Few rows of a: a workgroup takes 16 * NT rows of b and 16 * MT rows of a, its
 // waves share out k in steps of 128 and add their results through LDS.  The
-// operands go from memory to registers; each weight is read once.
-constexpr int kRowsWaves = 4;
+// operands go from memory to registers; each weight is read once, and every
+// workgroup reads its rows of a.  U steps' loads go out together: a wave has few
+// steps, and each round trip to memory costs as much as all of them.
+constexpr int kRowsWaves = 8;
 
-// U steps' loads go out together: a wave has few steps, and each round trip to
-// memory costs as much as all of them.
-template <bool FP4B, bool FP4A, int MT, int U>
+template <bool FP4B, bool FP4A, int NT, int MT, int U>
 __global__ __launch_bounds__(64 * kRowsWaves) void k_mx_matmul_rows(MatmulArgs A, int tiles_n) {
-    __shared__ v4f part[kRowsWaves][MT][64];
+    constexpr int W = kRowsWaves;
+    __shared__ v4f part[W][NT * MT][64];
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, g = lane >> 4, r = lane & 15;
     const int tile_m = blockIdx.x / tiles_n, tile_n = blockIdx.x - tile_m * tiles_n;
-    const int n = tile_n * 16 + r;
-    const bool in_n = n < A.N;
-    const int64_t nr = in_n ? n : 0;
-    const uint8_t* b = A.b + nr * row_bytes<FP4B>(A.K);
-    const uint8_t* be = A.be + nr * (A.K / 32);
-    const uint8_t *a[MT], *ae[MT];
-    bool in_m[MT];
-    v4f c[MT];
+    const uint8_t *a[MT], *ae[MT], *b[NT], *be[NT];
+    bool in_m[MT], in_n[NT];
+    v4f c[NT][MT];
+#pragma unroll
+    for (int j = 0; j < NT; j++) {
+        const int64_t n = ((int64_t)tile_n * NT + j) * 16 + r;
+        in_n[j] = n < A.N;
+        b[j] = A.b + (in_n[j] ? n : 0) * row_bytes<FP4B>(A.K);
+        be[j] = A.be + (in_n[j] ? n : 0) * (A.K / 32);
+    }
 #pragma unroll
     for (int i = 0; i < MT; i++) {
         const int64_t m = ((int64_t)tile_m * MT + i) * 16 + r;
         in_m[i] = m < A.M;
         a[i] = A.a + (in_m[i] ? m : 0) * row_bytes<FP4A>(A.K);
         ae[i] = A.ae + (in_m[i] ? m : 0) * (A.K / 32);
-        c[i] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int j = 0; j < NT; j++) c[j][i] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
     }
-    for (int k = wave * 128; k < A.K; k += kRowsWaves * 128 * U) {
-        Frag<FP4B> fb[U];
+    for (int k = wave * 128; k < A.K; k += W * 128 * U) {
+        Frag<FP4B> fb[U][NT];
         Frag<FP4A> fa[U][MT];
 #pragma unroll
         for (int u = 0; u < U; u++) {
-            const int k0 = k + u * kRowsWaves * 128;
-            fb[u] = load_frag<FP4B>(b, be, in_n, k0, A.K, g);
+            const int k0 = k + u * W * 128;
+#pragma unroll
+            for (int j = 0; j < NT; j++) fb[u][j] = load_frag<FP4B>(b[j], be[j], in_n[j], k0, A.K, g);
 #pragma unroll
             for (int i = 0; i < MT; i++) fa[u][i] = load_frag<FP4A>(a[i], ae[i], in_m[i], k0, A.K, g);
         }
 #pragma unroll
         for (int u = 0; u < U; u++)
 #pragma unroll
-            for (int i = 0; i < MT; i++) c[i] = mfma<FP4B, FP4A>(fb[u], fa[u][i], c[i]);
+            for (int j = 0; j < NT; j++)
+#pragma unroll
+                for (int i = 0; i < MT; i++) c[j][i] = mfma<FP4B, FP4A>(fb[u][j], fa[u][i], c[j][i]);
     }
 #pragma unroll
-    for (int i = 0; i < MT; i++) part[wave][i][lane] = c[i];
-    __syncthreads();
-    for (int i = wave; i < MT; i += kRowsWaves) {
-        v4f s = part[0][i][lane];
+    for (int j = 0; j < NT; j++)
 #pragma unroll
-        for (int w = 1; w < kRowsWaves; w++) s += part[w][i][lane];
-        const int64_t m = ((int64_t)tile_m * MT + i) * 16 + r;
-        const int at = tile_n * 16 + g * 4;
-        if (m < A.M && at < A.N) store_y4(A, m, at, s);
+        for (int i = 0; i < MT; i++) part[wave][j * MT + i][lane] = c[j][i];
+    __syncthreads();
+    for (int x = wave; x < NT * MT; x += W) {
+        v4f s = part[0][x][lane];
+#pragma unroll
+        for (int w = 1; w < W; w++) s += part[w][x][lane];
+        const int64_t m = ((int64_t)tile_m * MT + x % MT) * 16 + r, n = ((int64_t)tile_n * NT + x / MT) * 16 + g * 4;
+        if (m < A.M && n < A.N) store_y4(A, m, (int)n, s);
     }
 }
 
@@ -220,13 +228,15 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void k_mx_matmul_tile(MatmulArgs A
     constexpr int CB = PB / 16, CA = PA / 16;                  // 16-byte pieces of a row
     constexpr int LB = TN * CB / T, LA = TM * CA / T;          // loads of a thread
     constexpr int FN = TN / WN / 16, FM = TM / WM / 16;        // 16-row pieces of a wave
-    constexpr int SR = (TN + TM) / T;                          // scale rows of a thread
+    // scale rows are loaded 64 to a wave: of b by 64, of a by 64 or by wave where that is fewer
+    constexpr int kRowsA = FM < 4 ? FM * 16 : 64, kChunksB = TN / 64, kChunks = kChunksB + TM / kRowsA;
+    constexpr int SR = kChunks * 64 / T;                       // scale rows of a thread
     constexpr int kGroup = 4 / KS;                             // stages whose scale bytes come at once
     static_assert(TN * CB % T == 0 && TM * CA % T == 0 && (T / CB) % 16 == 0 && (T / CA) % 16 == 0, "whole loads, one swizzle per lane");
-    static_assert(TN % 64 == 0 && TM % 64 == 0 && (TN + TM) % T == 0 && FN % 4 == 0, "whole scale rows and result rows");
+    static_assert(TN % 64 == 0 && TM % kRowsA == 0 && kChunks * 64 % T == 0 && FN % 4 == 0, "whole scale rows and result rows");
     // LDS: two stages of codes a power of two apart, so that an address goes from one to the
     // other by flipping a bit; two groups of scale bytes; 2 KB of each wave's own for results
-    constexpr int kCodes = TN * PB + TM * PA, kScales = (TN + TM) * 16;
+    constexpr int kCodes = TN * PB + TM * PA, kScales = kChunks * 1024;
     constexpr int kNextCodes = 1 << (32 - __builtin_clz(kCodes - 1));
     constexpr int kScales0 = kNextCodes + kCodes, kOut = kScales0 + 2 * kScales;
     __shared__ __align__(4096) uint8_t lds[kOut + WN * WM * 2048];
@@ -246,7 +256,6 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void k_mx_matmul_tile(MatmulArgs A
     const int src_b = (tid % CB) ^ Stage<FP4B>::template swizzle<KS>(tid / CB);
     const int src_a = (tid % CA) ^ Stage<FP4A>::template swizzle<KS>(tid / CA);
     const uint32_t off_b = (uint32_t)(tid / CB) * pitch_b + src_b * 16, off_a = (uint32_t)(tid / CA) * pitch_a + src_a * 16;
-    const uint32_t off_s = (uint32_t)lane * blocks;
     const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) void*)lds;
 
     // The last tile of a row or column ends with the matrix: it repeats some of its neighbour's
@@ -261,15 +270,19 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void k_mx_matmul_tile(MatmulArgs A
     const int first_tile = run + blockIdx.x / kXcds;
     int load_tile = first_tile, load_step = 0;
     const uint8_t *gb = nullptr, *ga = nullptr, *gs[SR] = {};
+    uint32_t off_s[SR];
+#pragma unroll
+    for (int i = 0; i < SR; i++)
+        off_s[i] = (uint32_t)(i * T / 64 + wave < kChunksB ? lane : min(lane, kRowsA - 1)) * blocks;
     auto open_tile = [&]() {
         int64_t n0, m0;
         origin(load_tile, n0, m0);
         gb = A.b + n0 * pitch_b;
         ga = A.a + m0 * pitch_a;
 #pragma unroll
-        for (int i = 0; i < SR; i++) {   // a wave's 64 scale rows are all of b or all of a
-            const int first = i * T + wave * 64;
-            gs[i] = first < TN ? A.be + (n0 + first) * blocks : A.ae + (m0 + first - TN) * blocks;
+        for (int i = 0; i < SR; i++) {
+            const int chunk = i * T / 64 + wave;
+            gs[i] = chunk < kChunksB ? A.be + (n0 + chunk * 64) * blocks : A.ae + (m0 + (chunk - kChunksB) * kRowsA) * blocks;
         }
     };
     // Scale bytes come 16 to a row, enough for kGroup stages: a row's bytes lie far from
@@ -281,7 +294,7 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void k_mx_matmul_tile(MatmulArgs A
     auto load_scales = [&](int group) {
         if (blocks >= 16) {
 #pragma unroll
-            for (int i = 0; i < SR; i++) __builtin_memcpy(&sc[i], gs[i] + group_start(group) + off_s, 16);
+            for (int i = 0; i < SR; i++) __builtin_memcpy(&sc[i], gs[i] + group_start(group) + off_s[i], 16);
         } else {
 #pragma unroll
             for (int i = 0; i < SR; i++) {
@@ -290,7 +303,7 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void k_mx_matmul_tile(MatmulArgs A
                 for (int j = 0; j < 4; j++) {
                     w[j] = 0;
 #pragma unroll
-                    for (int x = 0; x < 4; x++) w[j] |= (uint32_t)gs[i][off_s + (4 * j + x < blocks ? 4 * j + x : 0)] << (8 * x);
+                    for (int x = 0; x < 4; x++) w[j] |= (uint32_t)gs[i][off_s[i] + (4 * j + x < blocks ? 4 * j + x : 0)] << (8 * x);
                 }
                 sc[i] = v4u{w[0], w[1], w[2], w[3]};
             }
@@ -363,7 +376,7 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void k_mx_matmul_tile(MatmulArgs A
         for (int x = 0; x < KS; x++) {
             const int y = min(at - start + x * 4 + g, last);
             sb[x] = to + wn * FN * 256 + y * 64;
-            sa[x] = to + TN * 16 + wm * FM * 256 + y * 64;
+            sa[x] = to + kChunksB * 1024 + wm * (TM / WM / kRowsA) * 1024 + y * 64;
         }
     };
     constexpr int SB = FN / 4, SA = (FM + 3) / 4;

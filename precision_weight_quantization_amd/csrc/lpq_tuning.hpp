@@ -195,14 +195,3 @@
 #ifndef LPQ_MX4QDQ_AHEAD
 #define LPQ_MX4QDQ_AHEAD 1
 #endif
-// Microscaled product of few rows: steps of 128 elements whose loads go out
-// together, for 16, 32 and 64 rows a workgroup.
-#ifndef LPQ_ROWS_U1
-#define LPQ_ROWS_U1 4
-#endif
-#ifndef LPQ_ROWS_U2
-#define LPQ_ROWS_U2 2
-#endif
-#ifndef LPQ_ROWS_U4
-#define LPQ_ROWS_U4 2
-#endif
