@@ -1,5 +1,9 @@
 // MXFP4: quantize (default and floor exponent rules), dequantize and QDQ.
 //
+// Streaming work bound by memory: 2 bytes in and 17/32 out an element, or the
+// other way round.  Measured at 9728 x 2560 (64 MB): quantize 12.3 us, dequantize
+// 12.2 us (5.2 TB/s, the rate of a large copy).
+//
 // Part of lpq_kernels.hip, which includes each part once, in this order: one
 // translation unit.
 #pragma once

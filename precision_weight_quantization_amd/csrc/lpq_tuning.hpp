@@ -167,9 +167,10 @@
 #ifndef LPQ_RQN_T
 #define LPQ_RQN_T LPQ_FLAT_THREADS
 #endif
-// MXFP4 codec (vectors per lane, workgroup size, load order).
+// MXFP4 codec (vectors per lane, workgroup size, load order): 128 threads of 4 vectors take 12.2 us
+// for 9728 x 2560 both ways, other shapes (1, 2 or 4 vectors, 128 to 512 threads) 12.2 to 13.9.
 #ifndef LPQ_MX4Q_U
-#define LPQ_MX4Q_U 2
+#define LPQ_MX4Q_U 4
 #endif
 #ifndef LPQ_MX4Q_T
 #define LPQ_MX4Q_T 128
@@ -178,16 +179,16 @@
 #define LPQ_MX4Q_AHEAD 1
 #endif
 #ifndef LPQ_MX4D_U
-#define LPQ_MX4D_U 2
+#define LPQ_MX4D_U 4
 #endif
 #ifndef LPQ_MX4D_T
-#define LPQ_MX4D_T 512
+#define LPQ_MX4D_T 128
 #endif
 #ifndef LPQ_MX4D_AHEAD
 #define LPQ_MX4D_AHEAD 0
 #endif
 #ifndef LPQ_MX4QDQ_U
-#define LPQ_MX4QDQ_U 2
+#define LPQ_MX4QDQ_U 4
 #endif
 #ifndef LPQ_MX4QDQ_T
 #define LPQ_MX4QDQ_T 128
