@@ -527,7 +527,7 @@ lpq_status lpq_rmsnorm_backward(const uint16_t* dy, const uint16_t* h, const uin
  * a [M, K]: activations (or a gradient), b [N, K]: weights (or the other
  * operand), each MXFP8 (codes [., K]) or MXFP4 (packed [., K/2]) with scale
  * bytes ae [M, K/32], be [N, K/32], as the quantizers above write them.  K % 32
- * == 0; any M and N; each below 2^31 - 1024, no operand or result above 2^40
+ * == 0; any M and N; each at most 2^30, no operand or result above 2^40
  * elements.  Codes and y 16-byte aligned, scale bytes any.
  * y [M, N]: LPQ_BF16, or LPQ_F32 when both operands are MXFP4 (the matrix
  * instruction sums E2M1 products exactly; with an E4M3 operand it drops what

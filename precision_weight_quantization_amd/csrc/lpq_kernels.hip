@@ -903,7 +903,7 @@ lpq_status lpq_rmsnorm_backward(const uint16_t* dy, const uint16_t* h, const uin
 
 lpq_status lpq_mx_matmul(const uint8_t* a, const uint8_t* ae, int a_format, const uint8_t* b, const uint8_t* be, int b_format,
                          int64_t M, int64_t N, int64_t K, void* y, int y_type, void* stream) {
-    const int64_t most = (int64_t(1) << 31) - 1024;   // tile and element offsets inside a row stay 32-bit
+    const int64_t most = int64_t(1) << 30;   // indexes along a row, some steps past its end too, stay 32-bit
     if (M <= 0 || N <= 0 || K <= 0 || K % 32 || M > most || N > most || K > most) return LPQ_ERR_SHAPE;
     if (M > (int64_t(1) << 40) / N || M > (int64_t(1) << 40) / K || N > (int64_t(1) << 40) / K) return LPQ_ERR_SHAPE;
     if (!a || !ae || !b || !be || !y) return LPQ_ERR_NULL;

@@ -32,37 +32,38 @@ def lpq():
 
 
 def operand(rows, K, fmt, seed, scale=1.0, outliers=1e-3):
-    """(codes as held, scale bytes, 64-bit values) of seeded normal data, some far out."""
+    """(codes as held, scale bytes, 64-bit values on the device) of seeded normal data, some far out."""
     rng = np.random.default_rng(seed)
     x = rng.standard_normal((rows, K)) * scale
     x = np.where(rng.random((rows, K)) < outliers, x * 50, x)
     codes, e = R.quantize(R.bf16_to_f64(R.f64_to_bf16(x)), fmt)
     held = R.pack(codes) if fmt == R.FP4 else codes
     t = torch.from_numpy(held).to(DEV)
-    return (t if fmt == R.FP4 else t.view(torch.float8_e4m3fn)), torch.from_numpy(e).to(DEV), R.values(codes, e, fmt)
+    return ((t if fmt == R.FP4 else t.view(torch.float8_e4m3fn)), torch.from_numpy(e).to(DEV),
+            torch.from_numpy(R.values(codes, e, fmt)).to(DEV))
 
 
 def bound(va, vb, exact, fmts, f32):
+    """The tolerance of each result, from 64-bit tensors or arrays of the operands' values and products."""
+    va, vb, exact = (torch.as_tensor(t) for t in (va, vb, exact))
     K = va.shape[1]
-    tol = (K / 128 + 8) * 2.0 ** -24 * (np.abs(va) @ np.abs(vb).T)
+    tol = (K / 128 + 8) * 2.0 ** -24 * (va.abs() @ vb.abs().T)
     if R.FP8 in fmts:
         for k in range(0, K, 128):
-            top = np.abs(va[:, k:k + 128]).max(1)[:, None] * np.abs(vb[:, k:k + 128]).max(1)[None, :]
-            tol += 128 * 2.0 ** -16 * top
-    return tol if f32 else tol + 2.0 ** -8 * (np.abs(exact) + tol)
+            tol += 128 * 2.0 ** -16 * torch.outer(va[:, k:k + 128].abs().amax(1), vb[:, k:k + 128].abs().amax(1))
+    return tol if f32 else tol + 2.0 ** -8 * (exact.abs() + tol)
 
 
 def check(lpq, A, B, fmts, f32, **kw):
     (a, ae, va), (b, be, vb) = A, B
     y = lpq.lpq_mx_matmul(a, ae, b, be, out_dtype=torch.float32 if f32 else torch.bfloat16, **kw)
     exact = va @ vb.T
-    err = np.abs(y.double().cpu().numpy() - exact)
-    tol = bound(va, vb, exact, fmts, f32)
-    assert np.isfinite(err).all() and (err <= tol).all(), (err.max(), (err / np.maximum(tol, 1e-300)).max())
+    err, tol = (y.double() - exact).abs(), bound(va, vb, exact, fmts, f32)
+    assert bool(torch.isfinite(err).all()) and bool((err <= tol).all()), (float(err.max()), float((err / tol).max()))
     # over many results far nearer than the worst case: BF16's error is 2^-9 on average
-    rel = np.linalg.norm(err) / max(np.linalg.norm(exact), 1e-300)
+    rel = float(err.norm() / exact.norm().clamp(min=1e-300))
     print(f"  relative error {rel:.3g}", flush=True)
-    assert exact.size < 256 or rel <= (1e-6 if f32 else 2.0 ** -8)
+    assert exact.numel() < 256 or rel <= (1e-6 if f32 else 2.0 ** -8)
     return y
 
 
@@ -79,12 +80,37 @@ def test_shapes(lpq, shape, fmts):
         check(lpq, A, B, fmts, True)
 
 
+# 128 x 128 tiles (one and several a workgroup), 256 x 192, 256 x 256 (one and several): whole and
+# ragged, k of two stages, of a part of a stage, of one scale group and of several
+TILED = [(1024, 1024, 256), (1000, 1100, 288), (1027, 1031, 416), (1024, 1032, 992), (4200, 4200, 160), (4000, 2600, 544),
+         (4001, 2601, 288), (4096, 4096, 800), (4099, 4101, 544), (8192, 4608, 352), (8200, 4610, 1056)]
+
+
+@pytest.mark.parametrize("fmts", FORMATS)
+@pytest.mark.parametrize("shape", TILED)
+def test_tiles(lpq, shape, fmts):
+    M, N, K = shape
+    rng = torch.Generator(device=DEV).manual_seed(9)
+    ops = []
+    for rows, fmt, seed in ((M, fmts[0], 11), (N, fmts[1], 12)):   # 200 rows of drawn values, in a shuffled order
+        held, e, v = operand(200, K, fmt, seed, outliers=1e-3)
+        at = torch.randint(0, 200, (rows,), device=DEV, generator=rng)
+        held = held.view(torch.uint8)[at]
+        ops.append((held if fmt == R.FP4 else held.view(torch.float8_e4m3fn), e[at], v[at]))
+    print(f"  {shape} {fmts}", flush=True)
+    y = check(lpq, *ops, fmts, False)
+    again = lpq.lpq_mx_matmul(*ops[0][:2], *ops[1][:2])
+    assert torch.equal(y.view(torch.int16), again.view(torch.int16))
+    if fmts == (R.FP4, R.FP4):
+        check(lpq, *ops, fmts, True)
+
+
 @pytest.mark.parametrize("fmts", FORMATS)
 def test_exact_integers(lpq, fmts):
     """Small whole numbers under unit scales: every product and sum is exact, so the BF16
     result is the correctly rounded one, at sizes that end inside every tile."""
     rng = np.random.default_rng(3)
-    for M, N, K in ((1, 40, 96), (19, 70, 416), (150, 300, 288), (260, 520, 160)):
+    for M, N, K in ((1, 40, 96), (19, 70, 416), (150, 300, 288), (260, 520, 160), (1029, 1111, 416), (1280, 1280, 928)):
         out, vals = [], []
         for rows, fmt in ((M, fmts[0]), (N, fmts[1])):
             v = rng.integers(-1, 2, (rows, K)).astype(np.float64)
@@ -98,11 +124,11 @@ def test_exact_integers(lpq, fmts):
         assert np.array_equal(y.double().cpu().numpy(), want)
 
 
+@pytest.mark.parametrize("M,N,K", [(40, 72, 544), (1030, 1100, 544)])
 @pytest.mark.parametrize("fmts", FORMATS)
-def test_scales_and_zero_blocks(lpq, fmts):
+def test_scales_and_zero_blocks(lpq, fmts, M, N, K):
     """Scales far apart from block to block, blocks of zeros under the smallest scale byte, and a row
     that is zero everywhere: its results are zeros."""
-    M, N, K = 40, 72, 544
     res = []
     for rows, fmt, seed in ((M, fmts[0], 4), (N, fmts[1], 5)):
         codes, e, _ = operand(rows, K, fmt, seed, 1.0, 0.0)
@@ -116,15 +142,17 @@ def test_scales_and_zero_blocks(lpq, fmts):
         raw = R.unpack(held) if fmt == R.FP4 else held
         e = e.astype(np.uint8)
         t = torch.from_numpy(held).to(DEV)
-        res.append((t if fmt == R.FP4 else t.view(torch.float8_e4m3fn), torch.from_numpy(e).to(DEV), R.values(raw, e, fmt)))
+        res.append((t if fmt == R.FP4 else t.view(torch.float8_e4m3fn), torch.from_numpy(e).to(DEV),
+                    torch.from_numpy(R.values(raw, e, fmt)).to(DEV)))
     (a, ae, va), (b, be, vb) = res
-    y = lpq.lpq_mx_matmul(a, ae, b, be).double().cpu().numpy()
+    y = lpq.lpq_mx_matmul(a, ae, b, be).double()
     exact = va @ vb.T
-    assert (y[3] == 0).all() and (y[:, 3] == 0).all()
-    assert (np.abs(y - exact) <= bound(va, vb, exact, fmts, False)).all()
+    assert bool((y[3] == 0).all()) and bool((y[:, 3] == 0).all())
+    assert bool(((y - exact).abs() <= bound(va, vb, exact, fmts, False)).all())
 
 
-@pytest.mark.parametrize("shape", [(1, 37, 128), (33, 70, 160), (200, 301, 256), (260, 514, 384)])
+@pytest.mark.parametrize("shape", [(1, 37, 128), (33, 70, 160), (200, 301, 256), (260, 514, 384), (1027, 1032, 416),
+                                   (1100, 1033, 160), (4100, 2568, 288)])
 def test_nothing_outside_is_written(lpq, shape):
     M, N, K = shape
     (a, ae, _), (b, be, _) = operand(M, K, R.FP8, 6), operand(N, K, R.FP4, 7)

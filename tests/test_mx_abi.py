@@ -177,7 +177,8 @@ def test_matmul_validation(lib):
 
     for k in ("a", "ae", "b", "be", "y"):
         assert call(**{k: None}) == 1, k
-    for k, v in (("M", 0), ("N", -1), ("K", 0), ("K", 48), ("M", 1 << 31), ("N", 1 << 31), ("K", 1 << 31)):
+    for k, v in (("M", 0), ("N", -1), ("K", 0), ("K", 48), ("M", 1 << 31), ("N", 1 << 31), ("K", 1 << 31),
+                 ("M", (1 << 30) + 1), ("N", (1 << 30) + 1), ("K", (1 << 30) + 32)):
         assert call(**{k: v}) == 2, (k, v)
     assert call(M=1 << 21, N=1 << 21) == 2 and call(M=1 << 21, K=1 << 21) == 2 and call(N=1 << 21, K=1 << 21) == 2
     for k, v in (("fa", 2), ("fb", -1), ("type", 2), ("type", -1)):
