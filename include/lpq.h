@@ -1,7 +1,10 @@
 /*
  * lpq.h -- C ABI of the MI355X (gfx950) low-precision weight codec library
- * (liblpq.so): BF16 -> block-wise FP8 / MXFP8 / NVFP4 quantizers, their
- * dequantizers, and the NVFP4 fake-quant (quantize-dequantize, "QDQ").
+ * (liblpq.so): BF16 -> block-wise FP8 / MXFP8 / MXFP4 / NVFP4 quantizers,
+ * their dequantizers and fake-quants (quantize-dequantize, "QDQ"); and the
+ * microscaled linear layer: two-way quantization, the root-mean-square norm
+ * with MXFP8 output and its gradients, and products of MXFP8 and MXFP4
+ * matrices.
  *
  * What the calls compute (web pages, cited by title and section):
  *  - "Low Precision RL" (Miles documentation), "Choose a precision" table and

@@ -8,6 +8,11 @@ stream and returns the outputs.  BF16 data is a ``torch.bfloat16`` tensor (or
 its ``int16``/``uint16`` bit view), E4M3 codes come back as
 ``torch.float8_e4m3fn``, scale bytes and packed FP4 as ``torch.uint8``.
 
+The microscaled linear layer (``lpq_quantize_mxfp8_transposed``,
+``lpq_rmsnorm_mxfp8``, ``lpq_rmsnorm_backward``, ``lpq_mx_matmul`` and their
+like) allocates what it is not given on the stream that it launches on, and
+launches on the device of its tensors, whichever is current.
+
 If the library has not been built the import fails: there is no fallback.
 """
 from __future__ import annotations

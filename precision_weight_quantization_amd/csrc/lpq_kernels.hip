@@ -5,8 +5,10 @@
 // sections 2.3-2.5 and 3.3): block-wise FP8 (E4M3, FP32 scale per 128x128
 // tile), MXFP8 (E4M3, UE8M0 byte per 1x32 block) and NVFP4 (E2M1, E4M3 scale
 // per 1x16 block, FP32 global scale amax / 2688 shared by a sibling group),
-// plus the NVFP4 fake-quant.  All of it is streaming work bound by HBM
-// bandwidth: no kernel here is a contraction, so none uses MFMA.
+// plus the NVFP4 fake-quant; MXFP4 (E2M1, UE8M0 byte per 1x32 block).  The
+// codecs are streaming work bound by HBM bandwidth, and so are the two-way
+// quantizer and the root-mean-square norm of the quantized layer; its products
+// run on the matrix cores (lpq_mx_matmul.hpp).
 //
 // Launch shape.  A grouped call covers many tensors in one launch.  The grid
 // is one-dimensional and dense: the host lays the tensors' work units
@@ -15,7 +17,7 @@
 // from that table with scalar compares and one division, then reads the
 // descriptor into scalar registers.
 // No workgroup is launched without work.
-//  * MXFP8 / NVFP4 / INT4 are flat in memory (N is a multiple of the block),
+//  * MXFP8 / MXFP4 / NVFP4 / INT4 are flat in memory (N is a multiple of the block),
 //    so a workgroup (128, 256 or 512 threads, chosen per kernel) streams
 //    16-byte BF16 vectors, 8 elements per lane, U vectors per lane; a 1x32 block is a quad of lanes and a 1x16 block a pair,
 //    reduced with DPP lane permutations.  U is 2 to 4 (16 for the read-only
