@@ -23,7 +23,7 @@ namespace {
 // Sums: the instruction adds 128 products and the accumulator in one step.
 // E2M1 products are summed exactly; with an E4M3 operand it aligns them to the
 // largest and drops what lies about 2^-16 below it (relative error of a sum
-// over normal data 4e-6 to 3e-5, for any length), which is why a result with
+// over normal data 3e-6 to 3e-5 at lengths 128, 2560 and 16384), which is why a result with
 // an E4M3 operand is offered in BF16 only.
 typedef int v8i __attribute__((ext_vector_type(8)));
 typedef float v4f __attribute__((ext_vector_type(4)));
@@ -162,7 +162,9 @@ __global__ __launch_bounds__(64 * kRowsWaves) void k_mx_matmul_rows(MatmulArgs A
 // stages of the tiles form one sequence: the next tile's first two are on their
 // way before a tile's results are stored, so that the stores and the first loads
 // cost no time of their own (measured with a workgroup per tile: 20 us a tile
-// beside the 35 us of its products at k = 2560, MXFP8).
+// beside the 35 us of its products at k = 2560, MXFP8).  Measured: 8192 x 9728 x
+// 2560 in MXFP8 176 us, 2.3 PFLOP/s; 8192 x 8192 x 8192 419 us, 2.6 PFLOP/s, and
+// 288 to 293 us in MXFP4, 3.8 PFLOP/s.
 //
 // The loads go from memory to LDS without registers: a wave's 64 pieces of 16
 // bytes land one after the other, so the order inside a stage is chosen by

@@ -1,8 +1,8 @@
 // MXFP4: quantize (default and floor exponent rules), dequantize and QDQ.
 //
 // Streaming work bound by memory: 2 bytes in and 17/32 out an element, or the
-// other way round.  Measured at 9728 x 2560 (64 MB): quantize 12.3 us, dequantize
-// 12.2 us (5.2 TB/s, the rate of a large copy).
+// other way round.  Measured at 9728 x 2560 (64 MB): quantize 11.9 us, dequantize
+// 12.6 us (5.0 to 5.3 TB/s, the rate of a large copy).
 //
 // Part of lpq_kernels.hip, which includes each part once, in this order: one
 // translation unit.
