@@ -165,12 +165,15 @@ def _launch(fn, where: str, like, stream, *args) -> None:
 _HERE = contextlib.nullcontext()
 
 
-def _on(stream):
+def _on(stream, like):
     """Where a call allocates what it is not given: on the stream that it launches on, so
-    that the memory's earlier users are ordered before it and its later ones behind it."""
+    that the memory's earlier users are ordered before it and its later ones behind it.
+    A handle is a stream of the device of ``like``."""
     if stream is None:
         return _HERE
-    return torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream)))
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(getattr(stream, "cuda_stream", stream)), device=like.device)
+    return torch.cuda.stream(stream)
 
 
 def _ptr(t) -> int:
@@ -308,7 +311,7 @@ def lpq_dequantize_mxfp8(q, e, y=None, stream=None):
 def _mxfp4_quantize(fn, where, w, p, e, stream):
     w = _bf16_in(w, "w")
     M, N = w.shape
-    with _on(stream):
+    with _on(stream, w):
         p, e = _outs(w, (p, "p", M * (N // 2), (M, max(N // 2, 1)), torch.uint8, 1),
                      (e, "e", M * (N // 32), (M, max(N // 32, 1)), torch.uint8, 1))
     _launch(fn, where, w, stream, w.data_ptr(), M, N, p.data_ptr(), e.data_ptr())
@@ -330,7 +333,7 @@ def lpq_dequantize_mxfp4(p, e, y=None, stream=None):
     p = _codes_in(p, "p")
     M, N = p.shape[0], p.shape[1] * 2
     _arg(e, "e", p, M * (N // 32), esize=1)
-    with _on(stream):
+    with _on(stream, p):
         y = _out(y, "y", p, 2 * M * N, (M, N), torch.bfloat16, 2)
     _launch(_L.lpq_dequantize_mxfp4, "lpq_dequantize_mxfp4", p, stream, p.data_ptr(), e.data_ptr(), M, N, y.data_ptr())
     return y
@@ -339,7 +342,7 @@ def lpq_dequantize_mxfp4(p, e, y=None, stream=None):
 def _mxfp4_qdq(fn, where, x, y, stream):
     x = _bf16_in(x, "x")
     M, N = x.shape
-    with _on(stream):
+    with _on(stream, x):
         y = _out(y, "y", x, 2 * M * N, (M, N), torch.bfloat16, 2)
     _launch(fn, where, x, stream, x.data_ptr(), M, N, y.data_ptr())
     return y
@@ -368,7 +371,7 @@ def _mx_transposed(fn, where, per_byte, dtype, w, rows, floor, qt, et, q, e, str
     if rows:
         specs += [(q, "q", M * (N // per_byte), (M, max(N // per_byte, 1)), dtype, 1),
                   (e, "e", M * (N // 32), (M, max(N // 32, 1)), torch.uint8, 1)]
-    with _on(stream):
+    with _on(stream, w):
         qt, et, q, e = (_outs(w, *specs) + [None, None])[:4]
     _launch(fn, where, w, stream, w.data_ptr(), M, N, int(bool(floor)), _ptr(q), _ptr(e), qt.data_ptr(), et.data_ptr())
     return qt, et, q, e
@@ -589,7 +592,7 @@ def lpq_rmsnorm(x, gamma, eps=1e-6, residual=None, h=None, rstd=None, y=None, st
     specs = [(y, "y", 2 * M * N, (M, N), torch.bfloat16, 2), (rstd, "rstd", 4 * M, (M,), torch.float32, 4)]
     if residual is not None:
         specs.append((h, "h", 2 * M * N, (M, N), torch.bfloat16, 2))
-    with _on(stream):
+    with _on(stream, x):
         y, rstd, h = (_outs(x, *specs) + [None])[:3]
     _launch(_L.lpq_rmsnorm, "lpq_rmsnorm", x, stream, x.data_ptr(), _ptr(residual), gamma.data_ptr(), float(eps), M, N, _ptr(h),
             rstd.data_ptr(), y.data_ptr())
@@ -608,7 +611,7 @@ def lpq_rmsnorm_mxfp8(x, gamma, eps=1e-6, residual=None, h=None, rstd=None, y=No
              (rstd, "rstd", 4 * M, (M,), torch.float32, 4)]
     if residual is not None:
         specs.append((h, "h", 2 * M * N, (M, N), torch.bfloat16, 2))
-    with _on(stream):
+    with _on(stream, x):
         q, e, rstd, h = (_outs(x, *specs) + [None])[:4]
     _launch(_L.lpq_rmsnorm_mxfp8, "lpq_rmsnorm_mxfp8", x, stream, x.data_ptr(), _ptr(residual), gamma.data_ptr(), float(eps),
             M, N, _ptr(h), rstd.data_ptr(), _ptr(y), q.data_ptr(), e.data_ptr())
@@ -643,7 +646,7 @@ def lpq_rmsnorm_backward(dy, h, gamma, rstd, dres=None, dx=None, dgamma=None, ac
     specs = [(dx, "dx", 2 * M * N, (M, N), torch.bfloat16, 2)]
     if want_dgamma:
         specs.append((dgamma, "dgamma", 4 * N, (N,), torch.float32, 4))
-    with _on(stream):
+    with _on(stream, dy):
         dx, dgamma = (_outs(dy, *specs) + [None])[:2]
         if need and workspace is None:
             workspace = _empty((need,), torch.uint8, dy)
@@ -685,7 +688,7 @@ def lpq_mx_matmul(a, ae, b, be, out_dtype=torch.bfloat16, y=None, a_format=None,
     if out_dtype not in _MX_OUT:
         raise TypeError(f"out_dtype must be one of {[str(d) for d in _MX_OUT]}, got {out_dtype}")
     size = 4 if out_dtype == torch.float32 else 2
-    with _on(stream):
+    with _on(stream, a):
         y = _out(y, "y", a, size * M * N, (M, N), out_dtype, size)
     _launch(_L.lpq_mx_matmul, "lpq_mx_matmul", a, stream, a.data_ptr(), ae.data_ptr(), fa, b.data_ptr(), be.data_ptr(), fb,
             M, N, K, y.data_ptr(), _MX_OUT[out_dtype])

@@ -172,7 +172,7 @@ def test_stream_argument(lpq):
     want = lpq.lpq_mx_matmul(*a, *b)
     torch.cuda.synchronize()
     side = torch.cuda.Stream()
-    for stream in (side, side.cuda_stream):
+    for stream in (side, side.cuda_stream, 0):   # 0: the default stream
         b2 = lpq.lpq_quantize_mxfp4(s.w, stream=stream)
         q2 = lpq.lpq_rmsnorm_mxfp8(s.x, s.gamma, stream=stream)
         y2 = lpq.lpq_mx_matmul(*a, *b2, stream=stream)
