@@ -20,10 +20,16 @@ namespace {
 // of the second.  The weights (b) are the first operand, so that a lane holds 4
 // neighbouring columns of y.
 //
-// Sums: the instruction adds 128 products and the accumulator in one step.
-// E2M1 products are summed exactly; with an E4M3 operand it aligns them to the
-// largest and drops what lies about 2^-16 below it (relative error of a sum
-// over normal data 3e-6 to 3e-5 at lengths 128, 2560 and 16384), which is why a result with
+// Sums (measured with single products of chosen exponents).  Two E2M1 operands:
+// the 32 products of a block are added exactly, then block after block to the
+// accumulator, each an FP32 addition.  With an E4M3 operand: 8 consecutive products
+// (aligned groups of 8 along k) are added after each has been cut towards zero to a
+// multiple of 2^(X - 13), X the largest sum of two factors' exponents among the
+// group's nonzero products (a subnormal code counts with the exponent of the
+// smallest normal one); then group after group in FP32.  That is fewer bits than
+// FP32 inside a group, and the instruction offers no other form: on normal data a
+// result is off by 3e-6 to 3e-5 (lengths 128, 2560 and 16384), which BF16 hides,
+// but products 2^-13 below one that cancels elsewhere are lost.  So a result with
 // an E4M3 operand is offered in BF16 only.
 typedef int v8i __attribute__((ext_vector_type(8)));
 typedef float v4f __attribute__((ext_vector_type(4)));
