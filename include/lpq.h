@@ -73,8 +73,10 @@ typedef enum lpq_status {
     LPQ_ERR_NULL = 1,   /* a required pointer is NULL                                   */
     LPQ_ERR_SHAPE = 2,  /* M or N <= 0, N not a multiple of the block (32 MXFP8/4, 16
                            NVFP4), a tensor count <= 0, or a tensor beyond the size
-                           limits (M * N above 2^40 for every call; tighter limits are
-                           stated where a call has one)                                 */
+                           limits (M * N above 2^40 for every call; in the codecs a
+                           tensor that would take 2^32 threads or more: none of up to
+                           2^35 elements, in block FP8 none of up to 2^21 tiles;
+                           tighter limits are stated where a call has one)              */
     LPQ_ERR_ALIGN = 3,  /* a pointer is not aligned as required (see above)             */
     LPQ_ERR_GROUP = 4,  /* an NVFP4 sibling-group index is outside [0, n_groups)        */
     LPQ_ERR_HIP = 5,    /* a HIP launch failed; lpq_last_hip_error() holds the code     */

@@ -91,6 +91,10 @@ constexpr int int4_group(Kind k) {
 }
 
 // Shape and pointer checks of one tensor for one kind of call.
+int64_t units(Kind k, const lpq_tensor& t);
+int64_t units(Kind k, const lpq_requant_tensor& t);
+bool one_launch_holds(Kind k, int64_t units);
+
 lpq_status check_tensor(Kind k, const lpq_tensor& t, int32_t n_groups) {
     if (t.rows <= 0 || t.cols <= 0) return LPQ_ERR_SHAPE;
     if (t.rows > (int64_t(1) << 40) / t.cols) return LPQ_ERR_SHAPE;   // element count overflow guard
@@ -159,7 +163,7 @@ lpq_status check_tensor(Kind k, const lpq_tensor& t, int32_t n_groups) {
         break;
     default: return LPQ_ERR_ARG;
     }
-    return LPQ_OK;
+    return one_launch_holds(k, units(k, t)) ? LPQ_OK : LPQ_ERR_SHAPE;
 }
 
 lpq_status check_tensor(Kind k, const lpq_requant_tensor& t, int32_t n_groups) {
@@ -168,6 +172,7 @@ lpq_status check_tensor(Kind k, const lpq_requant_tensor& t, int32_t n_groups) {
     if (!t.src || !t.src_scale) return LPQ_ERR_NULL;
     if (k != RQ_AMAX && (!t.dst || !t.dst_scale)) return LPQ_ERR_NULL;
     if (t.reserved != 0) return LPQ_ERR_ARG;
+    if (!one_launch_holds(k, units(k, t))) return LPQ_ERR_SHAPE;
     if (k == RQ_FP8) return aligned(t.src_scale, 4) && aligned(t.dst_scale, 4) ? LPQ_OK : LPQ_ERR_ALIGN;
     if (t.cols % (k == RQ_MX ? 32 : 16)) return LPQ_ERR_SHAPE;
     if (t.rows >= (int64_t(1) << 31) || t.cols >= (int64_t(1) << 31) - kRqStepMax) return LPQ_ERR_SHAPE;
@@ -221,7 +226,48 @@ int64_t units(Kind k, const lpq_requant_tensor& t) {
     }
 }
 
-constexpr int64_t kMaxGridX = 0x7fffffffLL;
+// The most workgroups of a launch: the runtime takes fewer than 2^32 threads along a
+// grid's axis, and the kernels' workgroup indexes are 32-bit.
+constexpr int64_t max_groups(int threads) {
+    const int64_t n = 0xffffffffLL / threads;
+    return n < 0x7fffffffLL ? n : 0x7fffffffLL;
+}
+
+// Threads of a kind's workgroup, as dispatch() launches it.
+int group_threads(Kind k) {
+    switch (k) {
+    case FP8BLK_Q: return 256 * LPQ_TILEQ_TW;
+    case FP8BLK_QW: return 256 * LPQ_TILEQ_WIDE_TW;
+    case FP8BLK_DQ: return LPQ_TILED_THREADS;
+    case FP8BLK_DQF: return LPQ_DQF_T;
+    case MXFP8_Q:
+    case MXFP8_QF: return LPQ_MXQ_T;
+    case MXFP8_DQ: return LPQ_MXD_T;
+    case MXFP4_Q:
+    case MXFP4_QF: return LPQ_MX4Q_T;
+    case MXFP4_DQ: return LPQ_MX4D_T;
+    case MXFP4_QDQ:
+    case MXFP4_QDQF: return LPQ_MX4QDQ_T;
+    case NV_AMAX: return LPQ_AMAX_T;
+    case NV_Q: return LPQ_NVQ_T;
+    case NV_DQ: return LPQ_NVD_T;
+    case NV_QDQ: return LPQ_QDQ_T;
+    case NV_QDQ_W: return LPQ_QDQW_T;
+    case I4_Q32:
+    case I4_Q128: return LPQ_I4Q_T;
+    case I4_DQ32:
+    case I4_DQ128: return LPQ_I4D_T;
+    case I4_QDQ32:
+    case I4_QDQ128: return LPQ_I4QDQ_T;
+    case RQ_FP8: return 256 * LPQ_RQT_TW;
+    case RQ_MX: return LPQ_RQM_T;
+    case RQ_AMAX: return LPQ_RQA_T;
+    case RQ_NV: return LPQ_RQN_T;
+    }
+    return 1024;
+}
+
+bool one_launch_holds(Kind k, int64_t units) { return units <= max_groups(group_threads(k)); }
 
 void dispatch(Kind k, dim3 grid, hipStream_t stream, const lpq_tensor* tab, const lpq_tensor& one, const ChunkMap& map,
               const float* fa, float* fb) {
@@ -312,17 +358,18 @@ void dispatch(Kind k, dim3 grid, hipStream_t stream, const lpq_requant_tensor* t
 }
 
 // Where the launch over tensors [i0, count) stops: the first tensor that would
-// exceed kMaxSeg segments (runs of equal work-unit counts) or 2^31-1 work units.
+// exceed kMaxSeg segments (runs of equal work-unit counts) or max_groups work units.
 // Fills map and total; returns -1 when one tensor alone is too large.
 template <typename D>
 int32_t slice_end(Kind k, const D* host, int32_t count, int32_t i0, const D& one, ChunkMap& map, int64_t& total) {
     map = ChunkMap{};
     total = 0;
+    const int64_t most = max_groups(group_threads(k));
     int32_t nseg = 0, i = i0;
     while (i < count) {
         const int64_t u = units(k, host ? host[i] : one);
-        if (u > kMaxGridX) return -1;
-        if (total + u > kMaxGridX) break;
+        if (u > most) return -1;
+        if (total + u > most) break;
         if (nseg == 0 || (int64_t)map.units[nseg - 1] != u) {
             if (nseg == kMaxSeg) break;
             map.first[nseg] = (uint32_t)total;
@@ -353,7 +400,7 @@ int64_t launch_count(Kind k, const D* host, int32_t n) {
 }
 
 // Launch kernel `k` over tensors [0, n) of `host`/`dev` (single tensor: dev ==
-// nullptr, `one` used), in slices of at most kMaxSeg segments and 2^31-1 work
+// nullptr, `one` used), in slices of at most kMaxSeg segments and max_groups work
 // units.
 template <typename D>
 lpq_status launch(Kind k, const D* host, const D* dev, int32_t n, const D& one, const float* fa, float* fb,
@@ -574,18 +621,22 @@ lpq_status mx_transpose(const uint16_t* w, int64_t M, int64_t N, int floor_rule,
         for (int j = 0; j < i; j++)
             if (overlap(out[i].p, out[i].n, out[j].p, out[j].n)) return LPQ_ERR_ARG;
     }
-    const int64_t tiles = (M + kTrM - 1) / kTrM * A.tiles_n;
-    if (tiles > kMaxGridX) return LPQ_ERR_SHAPE;
-    const dim3 grid((unsigned)tiles), block(kTrThreads);
+    const int64_t tiles = (M + kTrM - 1) / kTrM * A.tiles_n, most = max_groups(kTrThreads);
+    const dim3 block(kTrThreads);
     const hipStream_t s = (hipStream_t)stream;
-    if (floor_rule) {
-        if (q) hipLaunchKernelGGL((k_mx_transpose<FP4, true, true>), grid, block, 0, s, A);
-        else hipLaunchKernelGGL((k_mx_transpose<FP4, true, false>), grid, block, 0, s, A);
-    } else {
-        if (q) hipLaunchKernelGGL((k_mx_transpose<FP4, false, true>), grid, block, 0, s, A);
-        else hipLaunchKernelGGL((k_mx_transpose<FP4, false, false>), grid, block, 0, s, A);
+    for (A.first = 0; A.first < tiles; A.first += most) {
+        const dim3 grid((unsigned)(tiles - A.first < most ? tiles - A.first : most));
+        if (floor_rule) {
+            if (q) hipLaunchKernelGGL((k_mx_transpose<FP4, true, true>), grid, block, 0, s, A);
+            else hipLaunchKernelGGL((k_mx_transpose<FP4, true, false>), grid, block, 0, s, A);
+        } else {
+            if (q) hipLaunchKernelGGL((k_mx_transpose<FP4, false, true>), grid, block, 0, s, A);
+            else hipLaunchKernelGGL((k_mx_transpose<FP4, false, false>), grid, block, 0, s, A);
+        }
+        const lpq_status st = launched();
+        if (st != LPQ_OK) return st;
     }
-    return launched();
+    return LPQ_OK;
 }
 
 // Shape of a norm call: whole MXFP8 blocks, a row that fits the kernels' registers.
@@ -614,10 +665,24 @@ lpq_status rmsnorm(const NormArgs& A, void* stream) {
     }
     return by_row(A.N, [&](auto shape) {
         constexpr int G = decltype(shape)::g, U = decltype(shape)::u, kRows = norm_threads(G) / G;
-        const int64_t groups = (A.M + kRows - 1) / kRows;
-        if (groups > kMaxGridX) return LPQ_ERR_SHAPE;
-        hipLaunchKernelGGL((k_rmsnorm<G, U>), dim3((unsigned)groups), dim3(norm_threads(G)), 0, (hipStream_t)stream, A);
-        return launched();
+        constexpr int64_t most = max_groups(norm_threads(G)) * kRows;   // rows of a launch
+        for (int64_t row = 0; row < A.M; row += most) {
+            NormArgs S = A;
+            const int64_t at = row * A.N;
+            S.x += at;
+            if (S.residual) S.residual += at;
+            if (S.h) S.h += at;
+            if (S.y) S.y += at;
+            if (S.rstd) S.rstd += row;
+            if (S.q) S.q += at;
+            if (S.e) S.e += at / 32;
+            S.M = A.M - row < most ? A.M - row : most;
+            hipLaunchKernelGGL((k_rmsnorm<G, U>), dim3((unsigned)((S.M + kRows - 1) / kRows)), dim3(norm_threads(G)), 0,
+                               (hipStream_t)stream, S);
+            const lpq_status st = launched();
+            if (st != LPQ_OK) return st;
+        }
+        return LPQ_OK;
     });
 }
 
@@ -687,15 +752,20 @@ template <bool FP4A, bool FP4B>
 lpq_status mx_matmul(const MatmulArgs& A, hipStream_t s) {
     auto rows = [&](auto nt, auto mt, auto u) {
         constexpr int NT = decltype(nt)::value, MT = decltype(mt)::value, U = decltype(u)::value;
-        const int64_t tiles_n = ceil_div(A.N, 16 * NT), grid = ceil_div(A.M, 16 * MT) * tiles_n;
-        if (grid > kMaxGridX) return LPQ_ERR_SHAPE;
-        hipLaunchKernelGGL((k_mx_matmul_rows<FP4B, FP4A, NT, MT, U>), dim3((unsigned)grid), dim3(64 * kRowsWaves), 0, s, A, (int)tiles_n);
-        return launched();
+        const int64_t tiles_n = ceil_div(A.N, 16 * NT), tiles = ceil_div(A.M, 16 * MT) * tiles_n, most = max_groups(64 * kRowsWaves);
+        if (tiles > 0x7fffffffLL) return LPQ_ERR_SHAPE;   // tile indexes are 32-bit
+        for (int64_t first = 0; first < tiles; first += most) {
+            hipLaunchKernelGGL((k_mx_matmul_rows<FP4B, FP4A, NT, MT, U>), dim3((unsigned)(tiles - first < most ? tiles - first : most)),
+                               dim3(64 * kRowsWaves), 0, s, A, (int)tiles_n, (int)first);
+            const lpq_status st = launched();
+            if (st != LPQ_OK) return st;
+        }
+        return LPQ_OK;
     };
     auto tile = [&](auto tn, auto tm, auto wn, auto wm) {
         constexpr int TN = decltype(tn)::value, TM = decltype(tm)::value, WN = decltype(wn)::value, WM = decltype(wm)::value;
         const int64_t nt = ceil_div(A.N, TN), mt = ceil_div(A.M, TM);
-        if (nt * mt > kMaxGridX) return LPQ_ERR_SHAPE;
+        if (nt * mt > 0x7fffffffLL) return LPQ_ERR_SHAPE;   // tile indexes are 32-bit
         const int64_t most = kComputeUnits * (TN == 256 ? 1 : 2);   // as many as run at one time: they go on from tile to tile
         hipLaunchKernelGGL((k_mx_matmul_tile<FP4B, FP4A, TN, TM, WN, WM>), dim3((unsigned)(nt * mt < most ? nt * mt : most)),
                            dim3(64 * WN * WM), 0, s, A, (int)nt, (int)mt);
@@ -731,7 +801,7 @@ lpq_status observe_args(const uint16_t* x, int64_t M, int64_t N, int observer, c
     lpq_status st = check_tensor(NV_AMAX, *one, 0);   // same shape and alignment rules as the amax pass
     if (st != LPQ_OK) return st;
     *units = (M * N + chunk_elems<LPQ_AMAX_U>() - 1) / chunk_elems<LPQ_AMAX_U>();
-    return *units > kMaxGridX ? LPQ_ERR_SHAPE : LPQ_OK;
+    return *units > max_groups(kThreads) ? LPQ_ERR_SHAPE : LPQ_OK;
 }
 
 }  // namespace
@@ -812,7 +882,7 @@ lpq_status lpq_quantize_fp8blk(const uint16_t* w, int64_t M, int64_t N, uint8_t*
 
 lpq_status lpq_dequantize_fp8blk(const uint8_t* q, const float* s, int64_t M, int64_t N, uint16_t* y, void* stream) {
     const lpq_tensor one = make_one(q, y, const_cast<float*>(s), M, N);
-    const bool flat = check_tensor(FP8BLK_DQ, one, 0) == LPQ_OK && check_tensor(FP8BLK_DQF, one, 0) == LPQ_OK;
+    const bool flat = check_tensor(FP8BLK_DQF, one, 0) == LPQ_OK;   // with what FP8BLK_DQ asks for
     return single(flat ? FP8BLK_DQF : FP8BLK_DQ, one, nullptr, nullptr, stream);
 }
 

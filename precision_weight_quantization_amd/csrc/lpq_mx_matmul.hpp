@@ -105,11 +105,11 @@ __device__ __forceinline__ void store_y4(const MatmulArgs& A, int64_t m, int n, 
 constexpr int kRowsWaves = 8;
 
 template <bool FP4B, bool FP4A, int NT, int MT, int U>
-__global__ __launch_bounds__(64 * kRowsWaves) void k_mx_matmul_rows(MatmulArgs A, int tiles_n) {
+__global__ __launch_bounds__(64 * kRowsWaves) void k_mx_matmul_rows(MatmulArgs A, int tiles_n, int first) {
     constexpr int W = kRowsWaves;
     __shared__ v4f part[W][NT * MT][64];
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, g = lane >> 4, r = lane & 15;
-    const int tile_m = blockIdx.x / tiles_n, tile_n = blockIdx.x - tile_m * tiles_n;
+    const int tile = first + (int)blockIdx.x, tile_m = tile / tiles_n, tile_n = tile - tile_m * tiles_n;
     const uint8_t *a[MT], *ae[MT], *b[NT], *be[NT];
     bool in_m[MT], in_n[NT];
     v4f c[NT][MT];

@@ -33,6 +33,7 @@ struct TransposeArgs {
     int64_t M, N;
     int64_t Mp;          // M rounded up to a block
     int64_t tiles_n;
+    int64_t first;       // the launch's first tile
 };
 
 // Per-half maxima of two pairs of 16-bit magnitudes.
@@ -79,7 +80,7 @@ __global__ __launch_bounds__(kTrThreads) void k_mx_transpose(TransposeArgs A) {
     __shared__ __align__(16) uint8_t codes[kTrN * kPitch];
     __shared__ __align__(16) uint8_t scales[kTrN][kTrM / 32];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int64_t tile_m = blockIdx.x / A.tiles_n, tile_n = blockIdx.x - tile_m * A.tiles_n;
+    const int64_t tile = A.first + blockIdx.x, tile_m = tile / A.tiles_n, tile_n = tile - tile_m * A.tiles_n;
     const int64_t m0 = tile_m * kTrM, n0 = tile_n * kTrN;
     const int rr = lane >> 4, cc = lane & 15;
     const int64_t row = m0 + wave * 32 + rr * 8, col = n0 + cc * 8;
