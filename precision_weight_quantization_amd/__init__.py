@@ -8,10 +8,11 @@ stream and returns the outputs.  BF16 data is a ``torch.bfloat16`` tensor (or
 its ``int16``/``uint16`` bit view), E4M3 codes come back as
 ``torch.float8_e4m3fn``, scale bytes and packed FP4 as ``torch.uint8``.
 
-The microscaled linear layer (``lpq_quantize_mxfp8_transposed``,
-``lpq_rmsnorm_mxfp8``, ``lpq_rmsnorm_backward``, ``lpq_mx_matmul`` and their
-like) allocates what it is not given on the stream that it launches on, and
-launches on the device of its tensors, whichever is current.
+Every call launches on the device of its tensors or of its table, whichever is
+current.  With a ``stream`` argument the MXFP4 calls and the microscaled linear
+layer (``lpq_quantize_mxfp8_transposed``, ``lpq_rmsnorm_mxfp8``,
+``lpq_rmsnorm_backward``, ``lpq_mx_matmul`` and their like) allocate what they
+are not given on that stream, the others on the current one.
 
 If the library has not been built the import fails: there is no fallback.
 """
@@ -138,26 +139,27 @@ for _name, (_res, _args) in _SIG.items():
 EXPORTED = sorted(k for k in _SIG)
 
 
-def _check(status: int, where: str) -> None:
-    if status != LPQ_OK:
-        raise LpqError(status, where)
+def _current(index: int) -> int:
+    """The handle of the device's current stream, without a Stream object around it where torch offers that."""
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return raw(index) if raw is not None else torch.cuda.current_stream(index).cuda_stream
 
 
-def _stream(stream) -> int:
-    if stream is None:   # the current stream's handle, without a Stream object around it
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+def _stream(stream, index: int) -> int:
+    if stream is None:
+        return _current(index)
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def _launch(fn, where: str, like, stream, *args) -> None:
-    """Call ``fn(*args, stream)`` with the device of ``like`` current, on the given
-    stream or that device's current one."""
+    """Call ``fn(*args, stream)`` with the device of ``like`` (the call's data or table)
+    current, on the given stream or that device's current one."""
     index = like.device.index
     if index == torch.cuda.current_device():
-        status = fn(*args, torch._C._cuda_getCurrentRawStream(index) if stream is None else _stream(stream))
+        status = fn(*args, _stream(stream, index))
     else:
         with torch.cuda.device(index):
-            status = fn(*args, _stream(stream))
+            status = fn(*args, _stream(stream, index))
     if status != LPQ_OK:
         raise LpqError(status, where)
 
@@ -260,8 +262,7 @@ def lpq_quantize_fp8blk(w, q=None, s=None, stream=None):
     M, N = w.shape
     q, s = _outs(w, (q, "q", M * N, (M, N), torch.float8_e4m3fn, 1),
                  (s, "s", 4 * _tiles(M, N), fp8blk_scale_shape(M, N), torch.float32, 4))
-    _check(_L.lpq_quantize_fp8blk(w.data_ptr(), M, N, q.data_ptr(), s.data_ptr(), _stream(stream)),
-           "lpq_quantize_fp8blk")
+    _launch(_L.lpq_quantize_fp8blk, "lpq_quantize_fp8blk", w, stream, w.data_ptr(), M, N, q.data_ptr(), s.data_ptr())
     return q, s
 
 
@@ -270,8 +271,8 @@ def lpq_dequantize_fp8blk(q, s, y=None, stream=None):
     M, N = q.shape
     _arg(s, "s", q, 4 * _tiles(M, N), esize=4)
     y = _out(y, "y", q, 2 * M * N, (M, N), torch.bfloat16, 2)
-    _check(_L.lpq_dequantize_fp8blk(q.data_ptr(), s.data_ptr(), M, N, y.data_ptr(), _stream(stream)),
-           "lpq_dequantize_fp8blk")
+    _launch(_L.lpq_dequantize_fp8blk, "lpq_dequantize_fp8blk", q, stream, q.data_ptr(), s.data_ptr(), M, N,
+            y.data_ptr())
     return y
 
 
@@ -282,7 +283,7 @@ def _mxfp8_quantize(fn, where, w, q, e, stream):
     M, N = w.shape
     q, e = _outs(w, (q, "q", M * N, (M, N), torch.float8_e4m3fn, 1),
                  (e, "e", M * (N // 32), (M, max(N // 32, 1)), torch.uint8, 1))
-    _check(fn(w.data_ptr(), M, N, q.data_ptr(), e.data_ptr(), _stream(stream)), where)
+    _launch(fn, where, w, stream, w.data_ptr(), M, N, q.data_ptr(), e.data_ptr())
     return q, e
 
 
@@ -301,8 +302,7 @@ def lpq_dequantize_mxfp8(q, e, y=None, stream=None):
     M, N = q.shape
     _arg(e, "e", q, M * (N // 32), esize=1)
     y = _out(y, "y", q, 2 * M * N, (M, N), torch.bfloat16, 2)
-    _check(_L.lpq_dequantize_mxfp8(q.data_ptr(), e.data_ptr(), M, N, y.data_ptr(), _stream(stream)),
-           "lpq_dequantize_mxfp8")
+    _launch(_L.lpq_dequantize_mxfp8, "lpq_dequantize_mxfp8", q, stream, q.data_ptr(), e.data_ptr(), M, N, y.data_ptr())
     return y
 
 
@@ -399,8 +399,7 @@ def lpq_nvfp4_amax(w, amax=None, accumulate=False, stream=None):
     w = _bf16_in(w, "w")
     M, N = w.shape
     amax = _empty((1,), torch.float32, w) if amax is None else _f32_words(amax, "amax", w)
-    _check(_L.lpq_nvfp4_amax(w.data_ptr(), M, N, amax.data_ptr(), int(bool(accumulate)), _stream(stream)),
-           "lpq_nvfp4_amax")
+    _launch(_L.lpq_nvfp4_amax, "lpq_nvfp4_amax", w, stream, w.data_ptr(), M, N, amax.data_ptr(), int(bool(accumulate)))
     return amax
 
 
@@ -416,8 +415,8 @@ def lpq_quantize_nvfp4_ex(w, amax=None, e4m3_max=448, p=None, s=None, g=None, st
     p, s, g = _outs(w, (p, "p", M * (N // 2), (M, max(N // 2, 1)), torch.uint8, 1),
                     (s, "s", M * (N // 16), (M, max(N // 16, 1)), torch.float8_e4m3fn, 1),
                     (g, "g", 4, (1,), torch.float32, 4))
-    _check(_L.lpq_quantize_nvfp4_ex(w.data_ptr(), M, N, _ptr(amax), int(e4m3_max), p.data_ptr(), s.data_ptr(),
-                                    g.data_ptr(), _stream(stream)), "lpq_quantize_nvfp4_ex")
+    _launch(_L.lpq_quantize_nvfp4_ex, "lpq_quantize_nvfp4_ex", w, stream, w.data_ptr(), M, N, _ptr(amax), int(e4m3_max),
+            p.data_ptr(), s.data_ptr(), g.data_ptr())
     return p, s, g
 
 
@@ -432,8 +431,8 @@ def lpq_quantize_nvfp4(w, amax=None, p=None, s=None, g=None, stream=None):
     p, s, g = _outs(w, (p, "p", M * (N // 2), (M, max(N // 2, 1)), torch.uint8, 1),
                     (s, "s", M * (N // 16), (M, max(N // 16, 1)), torch.float8_e4m3fn, 1),
                     (g, "g", 4, (1,), torch.float32, 4))
-    _check(_L.lpq_quantize_nvfp4(w.data_ptr(), M, N, _ptr(amax), p.data_ptr(), s.data_ptr(), g.data_ptr(),
-                                 _stream(stream)), "lpq_quantize_nvfp4")
+    _launch(_L.lpq_quantize_nvfp4, "lpq_quantize_nvfp4", w, stream, w.data_ptr(), M, N, _ptr(amax), p.data_ptr(),
+            s.data_ptr(), g.data_ptr())
     return p, s, g
 
 
@@ -443,8 +442,8 @@ def lpq_nvfp4_qdq_ex(x, amax, e4m3_max=448, y=None, stream=None):
     if amax is not None:
         _f32_words(amax, "amax", x)
     y = _out(y, "y", x, 2 * M * N, (M, N), torch.bfloat16, 2)
-    _check(_L.lpq_nvfp4_qdq_ex(x.data_ptr(), M, N, _ptr(amax), int(e4m3_max), y.data_ptr(), _stream(stream)),
-           "lpq_nvfp4_qdq_ex")
+    _launch(_L.lpq_nvfp4_qdq_ex, "lpq_nvfp4_qdq_ex", x, stream, x.data_ptr(), M, N, _ptr(amax), int(e4m3_max),
+            y.data_ptr())
     return y
 
 
@@ -452,8 +451,8 @@ def lpq_nvfp4_global_scale_reciprocal(group_amax, out=None, stream=None):
     """fl(2688 / A) per group (the reciprocal export form of the global scale)."""
     _f32_words(group_amax, "group_amax", None, group_amax.numel() if isinstance(group_amax, torch.Tensor) else 1)
     out = torch.empty_like(group_amax) if out is None else _f32_words(out, "out", group_amax, group_amax.numel())
-    _check(_L.lpq_nvfp4_global_scale_reciprocal(group_amax.data_ptr(), group_amax.numel(), out.data_ptr(),
-                                                _stream(stream)), "lpq_nvfp4_global_scale_reciprocal")
+    _launch(_L.lpq_nvfp4_global_scale_reciprocal, "lpq_nvfp4_global_scale_reciprocal", group_amax, stream,
+            group_amax.data_ptr(), group_amax.numel(), out.data_ptr())
     return out
 
 
@@ -461,8 +460,8 @@ def lpq_nvfp4_global_scale(amax, out=None, stream=None):
     """fl(A / 2688) per entry (the multiplier form of a global scale)."""
     _f32_words(amax, "amax", None, amax.numel() if isinstance(amax, torch.Tensor) else 1)
     out = torch.empty_like(amax) if out is None else _f32_words(out, "out", amax, amax.numel())
-    _check(_L.lpq_nvfp4_global_scale(amax.data_ptr(), amax.numel(), out.data_ptr(), _stream(stream)),
-           "lpq_nvfp4_global_scale")
+    _launch(_L.lpq_nvfp4_global_scale, "lpq_nvfp4_global_scale", amax, stream, amax.data_ptr(), amax.numel(),
+            out.data_ptr())
     return out
 
 
@@ -477,7 +476,7 @@ def lpq_observer_reset(state=None, device=None, stream=None):
         state = torch.empty(OBSERVER_STATE_FLOATS, dtype=torch.float32, device=device or "cuda")
     else:
         _f32_words(state, "state", None, OBSERVER_STATE_FLOATS)
-    _check(_L.lpq_observer_reset(state.data_ptr(), _stream(stream)), "lpq_observer_reset")
+    _launch(_L.lpq_observer_reset, "lpq_observer_reset", state, stream, state.data_ptr())
     return state
 
 
@@ -488,8 +487,8 @@ def lpq_nvfp4_observe(x, state, observer="static_minmax", averaging_constant=0.0
     _f32_words(state, "state", x, OBSERVER_STATE_FLOATS)
     amax = _empty((1,), torch.float32, x) if amax is None else _f32_words(amax, "amax", x)
     kind = OBSERVERS[observer] if isinstance(observer, str) else int(observer)
-    _check(_L.lpq_nvfp4_observe(x.data_ptr(), M, N, kind, float(averaging_constant), state.data_ptr(),
-                                amax.data_ptr(), _stream(stream)), "lpq_nvfp4_observe")
+    _launch(_L.lpq_nvfp4_observe, "lpq_nvfp4_observe", x, stream, x.data_ptr(), M, N, kind, float(averaging_constant),
+            state.data_ptr(), amax.data_ptr())
     return amax
 
 
@@ -503,8 +502,8 @@ def lpq_nvfp4_observe_noalloc(x, state, observer="static_minmax", averaging_cons
     _f32_words(state, "state", x, 3)
     amax = _empty((1,), torch.float32, x) if amax is None else _f32_words(amax, "amax", x)
     kind = OBSERVERS[observer] if isinstance(observer, str) else int(observer)
-    _check(_L.lpq_nvfp4_observe_noalloc(x.data_ptr(), M, N, kind, float(averaging_constant), state.data_ptr(),
-                                        amax.data_ptr(), _stream(stream)), "lpq_nvfp4_observe_noalloc")
+    _launch(_L.lpq_nvfp4_observe_noalloc, "lpq_nvfp4_observe_noalloc", x, stream, x.data_ptr(), M, N, kind,
+            float(averaging_constant), state.data_ptr(), amax.data_ptr())
     return amax
 
 
@@ -514,8 +513,8 @@ def lpq_dequantize_nvfp4(p, s, g, y=None, stream=None):
     _arg(s, "s", p, M * (N // 16), esize=1)
     _f32_words(g, "g", p)
     y = _out(y, "y", p, 2 * M * N, (M, N), torch.bfloat16, 2)
-    _check(_L.lpq_dequantize_nvfp4(p.data_ptr(), s.data_ptr(), g.data_ptr(), M, N, y.data_ptr(), _stream(stream)),
-           "lpq_dequantize_nvfp4")
+    _launch(_L.lpq_dequantize_nvfp4, "lpq_dequantize_nvfp4", p, stream, p.data_ptr(), s.data_ptr(), g.data_ptr(), M, N,
+            y.data_ptr())
     return y
 
 
@@ -527,7 +526,7 @@ def lpq_nvfp4_qdq(x, amax=None, y=None, stream=None):
     if amax is not None:
         _f32_words(amax, "amax", x)
     y = _out(y, "y", x, 2 * M * N, (M, N), torch.bfloat16, 2)
-    _check(_L.lpq_nvfp4_qdq(x.data_ptr(), M, N, _ptr(amax), y.data_ptr(), _stream(stream)), "lpq_nvfp4_qdq")
+    _launch(_L.lpq_nvfp4_qdq, "lpq_nvfp4_qdq", x, stream, x.data_ptr(), M, N, _ptr(amax), y.data_ptr())
     return y
 
 
@@ -548,8 +547,8 @@ def lpq_quantize_int4(w, group=128, p=None, s=None, stream=None):
     G = _int4_group(group)
     p, s = _outs(w, (p, "p", M * (N // 2), (M, max(N // 2, 1)), torch.uint8, 1),
                  (s, "s", 4 * M * (N // G), (M, max(N // G, 1)), torch.float32, 4))
-    _check(_L.lpq_quantize_int4(w.data_ptr(), M, N, int(group), p.data_ptr(), s.data_ptr(), _stream(stream)),
-           "lpq_quantize_int4")
+    _launch(_L.lpq_quantize_int4, "lpq_quantize_int4", w, stream, w.data_ptr(), M, N, int(group), p.data_ptr(),
+            s.data_ptr())
     return p, s
 
 
@@ -558,8 +557,8 @@ def lpq_dequantize_int4(p, s, group=128, y=None, stream=None):
     M, N = p.shape[0], p.shape[1] * 2
     _arg(s, "s", p, 4 * M * (N // _int4_group(group)), esize=4)
     y = _out(y, "y", p, 2 * M * N, (M, N), torch.bfloat16, 2)
-    _check(_L.lpq_dequantize_int4(p.data_ptr(), s.data_ptr(), M, N, int(group), y.data_ptr(), _stream(stream)),
-           "lpq_dequantize_int4")
+    _launch(_L.lpq_dequantize_int4, "lpq_dequantize_int4", p, stream, p.data_ptr(), s.data_ptr(), M, N, int(group),
+            y.data_ptr())
     return y
 
 
@@ -568,7 +567,7 @@ def lpq_int4_qdq(x, group=128, y=None, stream=None):
     x = _bf16_in(x, "x")
     M, N = x.shape
     y = _out(y, "y", x, 2 * M * N, (M, N), torch.bfloat16, 2)
-    _check(_L.lpq_int4_qdq(x.data_ptr(), M, N, int(group), y.data_ptr(), _stream(stream)), "lpq_int4_qdq")
+    _launch(_L.lpq_int4_qdq, "lpq_int4_qdq", x, stream, x.data_ptr(), M, N, int(group), y.data_ptr())
     return y
 
 
@@ -705,8 +704,8 @@ def lpq_requantize_fp8blk(q, s, q_out=None, s_out=None, stream=None):
     _arg(s, "s", q, 4 * _tiles(M, N), esize=4)
     q_out, s_out = _outs(q, (q_out, "q_out", M * N, (M, N), torch.float8_e4m3fn, 1),
                          (s_out, "s_out", 4 * _tiles(M, N), fp8blk_scale_shape(M, N), torch.float32, 4))
-    _check(_L.lpq_requantize_fp8blk(q.data_ptr(), s.data_ptr(), M, N, q_out.data_ptr(), s_out.data_ptr(),
-                                    _stream(stream)), "lpq_requantize_fp8blk")
+    _launch(_L.lpq_requantize_fp8blk, "lpq_requantize_fp8blk", q, stream, q.data_ptr(), s.data_ptr(), M, N,
+            q_out.data_ptr(), s_out.data_ptr())
     return q_out, s_out
 
 
@@ -718,8 +717,8 @@ def lpq_requantize_fp8blk_mxfp8(q, s, q_out=None, e_out=None, stream=None):
     _arg(s, "s", q, 4 * _tiles(M, N), esize=4)
     q_out, e_out = _outs(q, (q_out, "q_out", M * N, (M, N), torch.float8_e4m3fn, 1),
                          (e_out, "e_out", M * (N // 32), (M, max(N // 32, 1)), torch.uint8, 1))
-    _check(_L.lpq_requantize_fp8blk_mxfp8(q.data_ptr(), s.data_ptr(), M, N, q_out.data_ptr(), e_out.data_ptr(),
-                                          _stream(stream)), "lpq_requantize_fp8blk_mxfp8")
+    _launch(_L.lpq_requantize_fp8blk_mxfp8, "lpq_requantize_fp8blk_mxfp8", q, stream, q.data_ptr(), s.data_ptr(), M, N,
+            q_out.data_ptr(), e_out.data_ptr())
     return q_out, e_out
 
 
@@ -729,8 +728,8 @@ def lpq_fp8blk_amax(q, s, amax=None, accumulate=False, stream=None):
     M, N = q.shape
     _arg(s, "s", q, 4 * _tiles(M, N), esize=4)
     amax = _empty((1,), torch.float32, q) if amax is None else _f32_words(amax, "amax", q)
-    _check(_L.lpq_fp8blk_amax(q.data_ptr(), s.data_ptr(), M, N, amax.data_ptr(), int(bool(accumulate)),
-                              _stream(stream)), "lpq_fp8blk_amax")
+    _launch(_L.lpq_fp8blk_amax, "lpq_fp8blk_amax", q, stream, q.data_ptr(), s.data_ptr(), M, N, amax.data_ptr(),
+            int(bool(accumulate)))
     return amax
 
 
@@ -744,9 +743,8 @@ def lpq_requantize_fp8blk_nvfp4(q, s, amax, p=None, sb=None, g=None, stream=None
     p, sb, g = _outs(q, (p, "p", M * (N // 2), (M, max(N // 2, 1)), torch.uint8, 1),
                      (sb, "sb", M * (N // 16), (M, max(N // 16, 1)), torch.float8_e4m3fn, 1),
                      (g, "g", 4, (1,), torch.float32, 4))
-    _check(_L.lpq_requantize_fp8blk_nvfp4(q.data_ptr(), s.data_ptr(), M, N, amax.data_ptr(), p.data_ptr(),
-                                          sb.data_ptr(), g.data_ptr(), _stream(stream)),
-           "lpq_requantize_fp8blk_nvfp4")
+    _launch(_L.lpq_requantize_fp8blk_nvfp4, "lpq_requantize_fp8blk_nvfp4", q, stream, q.data_ptr(), s.data_ptr(), M, N,
+            amax.data_ptr(), p.data_ptr(), sb.data_ptr(), g.data_ptr())
     return p, sb, g
 
 
@@ -866,58 +864,56 @@ def _group_words(t, name, table, n=None):
 
 
 def lpq_quantize_fp8blk_grouped(table: TensorTable, stream=None):
-    _check(_L.lpq_quantize_fp8blk_grouped(*table.check("fp8blk_q").args(), _stream(stream)),
-           "lpq_quantize_fp8blk_grouped")
+    _launch(_L.lpq_quantize_fp8blk_grouped, "lpq_quantize_fp8blk_grouped", table, stream,
+            *table.check("fp8blk_q").args())
 
 
 def lpq_dequantize_fp8blk_grouped(table: TensorTable, stream=None):
-    _check(_L.lpq_dequantize_fp8blk_grouped(*table.check("fp8blk_dq").args(), _stream(stream)),
-           "lpq_dequantize_fp8blk_grouped")
+    _launch(_L.lpq_dequantize_fp8blk_grouped, "lpq_dequantize_fp8blk_grouped", table, stream,
+            *table.check("fp8blk_dq").args())
 
 
 def lpq_quantize_mxfp8_grouped(table: TensorTable, stream=None):
-    _check(_L.lpq_quantize_mxfp8_grouped(*table.check("mxfp8_q").args(), _stream(stream)),
-           "lpq_quantize_mxfp8_grouped")
+    _launch(_L.lpq_quantize_mxfp8_grouped, "lpq_quantize_mxfp8_grouped", table, stream, *table.check("mxfp8_q").args())
 
 
 def lpq_quantize_mxfp8_floor_grouped(table: TensorTable, stream=None):
-    _check(_L.lpq_quantize_mxfp8_floor_grouped(*table.check("mxfp8_q").args(), _stream(stream)),
-           "lpq_quantize_mxfp8_floor_grouped")
+    _launch(_L.lpq_quantize_mxfp8_floor_grouped, "lpq_quantize_mxfp8_floor_grouped", table, stream,
+            *table.check("mxfp8_q").args())
 
 
 def lpq_dequantize_mxfp8_grouped(table: TensorTable, stream=None):
-    _check(_L.lpq_dequantize_mxfp8_grouped(*table.check("mxfp8_dq").args(), _stream(stream)),
-           "lpq_dequantize_mxfp8_grouped")
+    _launch(_L.lpq_dequantize_mxfp8_grouped, "lpq_dequantize_mxfp8_grouped", table, stream,
+            *table.check("mxfp8_dq").args())
 
 
 def lpq_quantize_mxfp4_grouped(table: TensorTable, stream=None):
-    _check(_L.lpq_quantize_mxfp4_grouped(*table.check("mxfp4_q").args(), _stream(stream)),
-           "lpq_quantize_mxfp4_grouped")
+    _launch(_L.lpq_quantize_mxfp4_grouped, "lpq_quantize_mxfp4_grouped", table, stream, *table.check("mxfp4_q").args())
 
 
 def lpq_quantize_mxfp4_floor_grouped(table: TensorTable, stream=None):
-    _check(_L.lpq_quantize_mxfp4_floor_grouped(*table.check("mxfp4_q").args(), _stream(stream)),
-           "lpq_quantize_mxfp4_floor_grouped")
+    _launch(_L.lpq_quantize_mxfp4_floor_grouped, "lpq_quantize_mxfp4_floor_grouped", table, stream,
+            *table.check("mxfp4_q").args())
 
 
 def lpq_dequantize_mxfp4_grouped(table: TensorTable, stream=None):
-    _check(_L.lpq_dequantize_mxfp4_grouped(*table.check("mxfp4_dq").args(), _stream(stream)),
-           "lpq_dequantize_mxfp4_grouped")
+    _launch(_L.lpq_dequantize_mxfp4_grouped, "lpq_dequantize_mxfp4_grouped", table, stream,
+            *table.check("mxfp4_dq").args())
 
 
 def lpq_mxfp4_qdq_grouped(table: TensorTable, stream=None):
-    _check(_L.lpq_mxfp4_qdq_grouped(*table.check("mxfp4_qdq").args(), _stream(stream)), "lpq_mxfp4_qdq_grouped")
+    _launch(_L.lpq_mxfp4_qdq_grouped, "lpq_mxfp4_qdq_grouped", table, stream, *table.check("mxfp4_qdq").args())
 
 
 def lpq_mxfp4_qdq_floor_grouped(table: TensorTable, stream=None):
-    _check(_L.lpq_mxfp4_qdq_floor_grouped(*table.check("mxfp4_qdq").args(), _stream(stream)),
-           "lpq_mxfp4_qdq_floor_grouped")
+    _launch(_L.lpq_mxfp4_qdq_floor_grouped, "lpq_mxfp4_qdq_floor_grouped", table, stream,
+            *table.check("mxfp4_qdq").args())
 
 
 def lpq_nvfp4_amax_grouped(table: TensorTable, group_amax, accumulate=False, stream=None):
     _group_words(group_amax, "group_amax", table)
-    _check(_L.lpq_nvfp4_amax_grouped(*table.check("nvfp4_amax").args(), group_amax.data_ptr(), group_amax.numel(),
-                                     int(bool(accumulate)), _stream(stream)), "lpq_nvfp4_amax_grouped")
+    _launch(_L.lpq_nvfp4_amax_grouped, "lpq_nvfp4_amax_grouped", table, stream, *table.check("nvfp4_amax").args(),
+            group_amax.data_ptr(), group_amax.numel(), int(bool(accumulate)))
     return group_amax
 
 
@@ -926,9 +922,8 @@ def lpq_quantize_nvfp4_grouped(table: TensorTable, group_amax, group_g, amax_val
     its group's slot) before it encodes."""
     _group_words(group_amax, "group_amax", table)
     _group_words(group_g, "group_g", table, group_amax.numel())
-    _check(_L.lpq_quantize_nvfp4_grouped(*table.check("nvfp4_q").args(), group_amax.data_ptr(), group_amax.numel(),
-                                         int(bool(amax_valid)), group_g.data_ptr(), _stream(stream)),
-           "lpq_quantize_nvfp4_grouped")
+    _launch(_L.lpq_quantize_nvfp4_grouped, "lpq_quantize_nvfp4_grouped", table, stream, *table.check("nvfp4_q").args(),
+            group_amax.data_ptr(), group_amax.numel(), int(bool(amax_valid)), group_g.data_ptr())
     return group_g
 
 
@@ -936,70 +931,67 @@ def lpq_quantize_nvfp4_grouped_ex(table: TensorTable, group_amax, group_g, e4m3_
                                   stream=None):
     _group_words(group_amax, "group_amax", table)
     _group_words(group_g, "group_g", table, group_amax.numel())
-    _check(_L.lpq_quantize_nvfp4_grouped_ex(*table.check("nvfp4_q").args(), group_amax.data_ptr(), group_amax.numel(),
-                                            int(bool(amax_valid)), int(e4m3_max), group_g.data_ptr(),
-                                            _stream(stream)), "lpq_quantize_nvfp4_grouped_ex")
+    _launch(_L.lpq_quantize_nvfp4_grouped_ex, "lpq_quantize_nvfp4_grouped_ex", table, stream,
+            *table.check("nvfp4_q").args(), group_amax.data_ptr(), group_amax.numel(), int(bool(amax_valid)),
+            int(e4m3_max), group_g.data_ptr())
     return group_g
 
 
 def lpq_nvfp4_qdq_grouped_ex(table: TensorTable, group_amax, e4m3_max=448, amax_valid=True, stream=None):
     _group_words(group_amax, "group_amax", table)
-    _check(_L.lpq_nvfp4_qdq_grouped_ex(*table.check("nvfp4_qdq").args(), group_amax.data_ptr(), group_amax.numel(),
-                                       int(bool(amax_valid)), int(e4m3_max), _stream(stream)),
-           "lpq_nvfp4_qdq_grouped_ex")
+    _launch(_L.lpq_nvfp4_qdq_grouped_ex, "lpq_nvfp4_qdq_grouped_ex", table, stream, *table.check("nvfp4_qdq").args(),
+            group_amax.data_ptr(), group_amax.numel(), int(bool(amax_valid)), int(e4m3_max))
 
 
 def lpq_dequantize_nvfp4_grouped(table: TensorTable, group_g, stream=None):
     _group_words(group_g, "group_g", table)
-    _check(_L.lpq_dequantize_nvfp4_grouped(*table.check("nvfp4_dq").args(), group_g.data_ptr(), group_g.numel(),
-                                           _stream(stream)), "lpq_dequantize_nvfp4_grouped")
+    _launch(_L.lpq_dequantize_nvfp4_grouped, "lpq_dequantize_nvfp4_grouped", table, stream,
+            *table.check("nvfp4_dq").args(), group_g.data_ptr(), group_g.numel())
 
 
 def lpq_nvfp4_qdq_grouped(table: TensorTable, group_amax, amax_valid=True, stream=None):
     """amax_valid False: the call fills group_amax before it encodes."""
     _group_words(group_amax, "group_amax", table)
-    _check(_L.lpq_nvfp4_qdq_grouped(*table.check("nvfp4_qdq").args(), group_amax.data_ptr(), group_amax.numel(),
-                                    int(bool(amax_valid)), _stream(stream)), "lpq_nvfp4_qdq_grouped")
+    _launch(_L.lpq_nvfp4_qdq_grouped, "lpq_nvfp4_qdq_grouped", table, stream, *table.check("nvfp4_qdq").args(),
+            group_amax.data_ptr(), group_amax.numel(), int(bool(amax_valid)))
 
 
 def lpq_quantize_int4_grouped(table: TensorTable, group=128, stream=None):
-    _check(_L.lpq_quantize_int4_grouped(*table.check("int4_q", _int4_group(group)).args(), int(group),
-                                        _stream(stream)), "lpq_quantize_int4_grouped")
+    _launch(_L.lpq_quantize_int4_grouped, "lpq_quantize_int4_grouped", table, stream,
+            *table.check("int4_q", _int4_group(group)).args(), int(group))
 
 
 def lpq_dequantize_int4_grouped(table: TensorTable, group=128, stream=None):
-    _check(_L.lpq_dequantize_int4_grouped(*table.check("int4_dq", _int4_group(group)).args(), int(group),
-                                          _stream(stream)), "lpq_dequantize_int4_grouped")
+    _launch(_L.lpq_dequantize_int4_grouped, "lpq_dequantize_int4_grouped", table, stream,
+            *table.check("int4_dq", _int4_group(group)).args(), int(group))
 
 
 def lpq_int4_qdq_grouped(table: TensorTable, group=128, stream=None):
-    _check(_L.lpq_int4_qdq_grouped(*table.check("int4_qdq").args(), int(group), _stream(stream)),
-           "lpq_int4_qdq_grouped")
+    _launch(_L.lpq_int4_qdq_grouped, "lpq_int4_qdq_grouped", table, stream, *table.check("int4_qdq").args(), int(group))
 
 
 def lpq_requantize_fp8blk_grouped(table: RequantTable, stream=None):
-    _check(_L.lpq_requantize_fp8blk_grouped(*table.check("rq_fp8").args(), _stream(stream)),
-           "lpq_requantize_fp8blk_grouped")
+    _launch(_L.lpq_requantize_fp8blk_grouped, "lpq_requantize_fp8blk_grouped", table, stream,
+            *table.check("rq_fp8").args())
 
 
 def lpq_requantize_fp8blk_mxfp8_grouped(table: RequantTable, stream=None):
-    _check(_L.lpq_requantize_fp8blk_mxfp8_grouped(*table.check("rq_mx").args(), _stream(stream)),
-           "lpq_requantize_fp8blk_mxfp8_grouped")
+    _launch(_L.lpq_requantize_fp8blk_mxfp8_grouped, "lpq_requantize_fp8blk_mxfp8_grouped", table, stream,
+            *table.check("rq_mx").args())
 
 
 def lpq_fp8blk_amax_grouped(table: RequantTable, group_amax, accumulate=False, stream=None):
     _group_words(group_amax, "group_amax", table)
-    _check(_L.lpq_fp8blk_amax_grouped(*table.check("rq_amax").args(), group_amax.data_ptr(), group_amax.numel(),
-                                      int(bool(accumulate)), _stream(stream)), "lpq_fp8blk_amax_grouped")
+    _launch(_L.lpq_fp8blk_amax_grouped, "lpq_fp8blk_amax_grouped", table, stream, *table.check("rq_amax").args(),
+            group_amax.data_ptr(), group_amax.numel(), int(bool(accumulate)))
     return group_amax
 
 
 def lpq_requantize_fp8blk_nvfp4_grouped(table: RequantTable, group_amax, group_g, stream=None):
     _group_words(group_amax, "group_amax", table)
     _group_words(group_g, "group_g", table, group_amax.numel())
-    _check(_L.lpq_requantize_fp8blk_nvfp4_grouped(*table.check("rq_nv").args(), group_amax.data_ptr(),
-                                                  group_amax.numel(), group_g.data_ptr(), _stream(stream)),
-           "lpq_requantize_fp8blk_nvfp4_grouped")
+    _launch(_L.lpq_requantize_fp8blk_nvfp4_grouped, "lpq_requantize_fp8blk_nvfp4_grouped", table, stream,
+            *table.check("rq_nv").args(), group_amax.data_ptr(), group_amax.numel(), group_g.data_ptr())
     return group_g
 
 
