@@ -535,8 +535,9 @@ lpq_status lpq_rmsnorm_backward(const uint16_t* dy, const uint16_t* h, const uin
  * == 0; any M and N; each at most 2^30, no operand or result above 2^40
  * elements.  Codes and y 16-byte aligned, scale bytes any.
  * y [M, N]: LPQ_BF16, or LPQ_F32 when both operands are MXFP4.  y may not overlap
- * an input (LPQ_ERR_ARG).  How the sums are taken, in a fixed order (a call's
- * result does not vary):
+ * an input (LPQ_ERR_ARG).  How the sums are taken, in an order fixed by the formats
+ * and M, N and K: a call's result does not vary, but a row's last bits may with the
+ * number of rows beside it (few rows and many are summed in different orders).
  *  - Two MXFP4 operands: the 32 products of a block exactly, the block sums in
  *    FP32.  Error: at most (K/32 + 8) * 2^-24 of the sum of |a b|.
  *  - With an MXFP8 operand: 8 consecutive products (aligned groups of 8 along k)
@@ -544,10 +545,10 @@ lpq_status lpq_rmsnorm_backward(const uint16_t* dy, const uint16_t* h, const uin
  *    2^(X - 13), X the largest sum of two factors' exponents among the group's
  *    nonzero products (a subnormal code counts with the exponent of the smallest
  *    normal one); the group sums in FP32.  A product of normal codes loses less
- *    than 2^-13 of the largest of its group.  Relative error of a result on normal
- *    data 3e-6 to 3e-5, below BF16's 2^-9; but where large products cancel, what
- *    small ones beside them would leave can be lost.  An FP32 result is refused
- *    (LPQ_ERR_ARG).
+ *    than 2^-13 of the largest of its group.  Results on normal data are off by
+ *    2e-6 to 2e-5 of their root mean square, with outliers by up to 6e-5, which
+ *    BF16's step hides; but where large products cancel, what small ones beside them
+ *    would leave can be lost.  An FP32 result is refused (LPQ_ERR_ARG).
  * NaN codes (0x7F, 0xFF) and scale byte 255 are outside the contract.
  * A layer's three products: forward y = x w^T (a = x, b = w, both in row form),
  * dx = dy w (a = dy, b = w transposed), dw = dy^T x (a = dy transposed, b = x

@@ -735,16 +735,24 @@ using Int = std::integral_constant<int, N>;
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// Which kernel a product takes.
-//  * Tiles of 128 x 128 or more by way of LDS, from 64 such tiles on: fewer leave
-//    most of the card idle, and a stage's way from memory to LDS takes as long for
-//    one tile as for 256 (measured, MXFP8 x MXFP4 at k = 2560: 128 x 2560 15 us as
-//    20 tiles and 10 by rows; 128 x 9728 18 us as 76 tiles and 36 by rows).
+// Which kernel a product takes.  Both sides were timed for the four format pairs
+// at k = 2560 and 9728; times here are us of MXFP8 / MXFP8 x MXFP4 / MXFP4.
+//  * Tiles of 128 x 128 or more by way of LDS, from 128 rows and 64 such tiles on:
+//    fewer leave most of the card idle, and a stage's way from memory to LDS takes as
+//    long for one tile as for 256.  128 x 9728 x 2560 (76 tiles): 18 / 17 / 12 in
+//    tiles, 28 / 24 / 19 by rows; 512 x 2560 x 9728 (80): 57 / 55 / 37 and 89 / 72 /
+//    56.  256 x 2560 (40): 18 / 17 / 12 in tiles, 15 / 13 / 11 by rows at k = 2560; 57 /
+//    55 / 37 and 46 / 37 / 29 at 9728.  A tile has 128 rows to itself, so 65 to 127
+//    rows go by rows where tiles might be faster: 127 x 9728 x 2560 takes 28 / 24 / 19.
 //  * Among the tiles the shape that takes the least time for its rounds of the
 //    card.  One round (256 tiles, one on each CU) of 256 x 256 counts 2; 256 x 192
 //    1.8; 128 x 128 0.95 alone, 1.1 with two on each CU, and 1.6 where many rounds
-//    keep memory busy, which larger tiles ask less of (measured at k = 2560, MXFP8:
-//    37 us, 33 us, 16 and 20 us, 28 us a round).
+//    keep memory busy, which larger tiles ask less of.  These are MXFP8's times at k =
+//    2560 (37 us, 33 us, 16 and 20 us, 28 us a round) and decide the other pairs and k
+//    too: of 14 sizes from 1024 x 2560 x 2560 to 8192 x 8192 x 8192 the choice is within
+//    10% of the fastest shape at 12; 2048 x 9728 x 9728 takes 256 / 210 / 155 by 128 x
+//    128 and 225 / 196 / 133 by 256 x 192, 8192 x 8192 x 512 52 / 49 / 41 by 256 x 256
+//    and 48 / 46 / 37 by 256 x 192.
 //  * Rows otherwise, in workgroups of as many rows of b as leave 128 workgroups: each
 //    reads its rows of a once (64 x 9728 x 2560: 23 us with 16, 19 with 32 and 14
 //    with 64; 64 x 2560 x 2560, 40 workgroups with 64: 9 us with 16, 12 with 64).

@@ -1,9 +1,13 @@
 // Two-way microscaled quantization: the blocks of a matrix along its rows
 // and, transposed, along its columns, from one read.
 //
-// Bound by memory.  Measured: 8192 x 2048 to both MXFP8 forms, 68 MB, 14.0 us
-// (4.8 TB/s; a 1 GiB copy reaches 5.1); 1237 x 7168 to the MXFP4 column form, 22 MB,
-// 7.4 us, where 560 workgroups are two on a CU and their loads' latency shows.
+// Bound by memory, and in small matrices by the latency of few workgroups.  Measured,
+// buffers larger than the memory-side cache (both forms / the column form alone; at the
+// 5.2 TB/s of a 1 GiB copy in brackets): 8192 x 2048 in MXFP8 17.3 / 12.6 us (13.2 / 9.8),
+// in MXFP4 16.5 / 12.3 (9.9 / 8.2); 1237 x 7168 in MXFP8 12.1 / 9.4 (7.0 / 5.2), in MXFP4
+// 10.8 / 8.0 (5.3 / 4.3).  There 560 workgroups of 128 x 128 are two on a CU and their
+// loads' latency shows; smaller tiles were not tried.  With 200 MB of buffers, part of
+// them still in the cache: 13.8 us for 8192 x 2048 in MXFP8, both forms.
 //
 // Part of lpq_kernels.hip, which includes each part once, in this order: one
 // translation unit.
@@ -88,7 +92,7 @@ __global__ __launch_bounds__(kTrThreads) void k_mx_transpose(TransposeArgs A) {
 
     // Plain loads: the producer has just written w, and what of it is still in the
     // memory-side cache counts (non-temporal loads: 17.9 us instead of 14.0 at 8192 x 2048
-    // from buffers of 100 MB together).
+    // from buffers of 100 MB together, a run before the figures above).
     v4u v[8];
 #pragma unroll
     for (int p = 0; p < 8; p++) {

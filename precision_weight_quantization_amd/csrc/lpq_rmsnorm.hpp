@@ -15,15 +15,21 @@ namespace {
 //   dx     = BF16(r * (g - n * sum(g * n) / N) + dres)
 //   dgamma = sum over the rows of dy * n         FP32
 //
-// Both read every array once and hold the row in registers between the
-// reduction and the result, so HBM traffic is the floor.  G threads share a
-// row, U vectors of 8 elements each: part of a wave for short rows (several
-// rows per wave), one wave up to 4096 elements (the row's sum is then lane
-// exchanges, without LDS or a barrier), a workgroup above.
-// Measured: 8192 x 2560 with a residual and MXFP8 output (147 MB) 28.4 us, 5.2
-// TB/s; its gradients (168 MB) 36.3 us, 4.6 TB/s, and 4.7 us for the sum of the
-// partials; 98301 x 128 gradients (76 MB) 15.6 us, 4.8 TB/s, and 3.9 us.  One row
-// of 2560 takes 3.8 us, a launch and a few round trips to memory.
+// Both read every array once, so HBM traffic is the floor, and work on a row out of
+// registers between the reduction and the result.  G threads share a row, U vectors
+// of 8 elements each: part of a wave for short rows (several rows per wave), one
+// wave up to 4096 elements (the row's sum is then lane exchanges, without LDS or a
+// barrier), a workgroup above.  The forward pass holds its rows without spilling.
+// The gradients do up to 8192 elements (one wave a SIMD with 256 registers and the
+// rest in accumulation registers from 2048 on); above, 1024 threads leave a lane 128
+// registers: <1024, 2> (up to 16384) spills 8 of them, <1024, 4> (up to 32768) 112.
+// Measured, with a residual, 168 MB (147 with MXFP8 output), buffers larger than
+// the memory-side cache: 8192 x 2560 norm with MXFP8 output 28.8 us, 5.1 TB/s, with
+// BF16 31.6; 2560 x 8192 28.7 and 30.0; 640 x 32768 32.0 and 32.4.  Gradients: 8192 x
+// 2560 34.3 us without dgamma, 39.0 with (36.0 + 4.1 by themselves); 2560 x 8192 34.3
+// and 40.8; 1280 x 16384 34.5 and 44.5; 640 x 32768 134 and 145, the spills.  98301 x
+// 128 gradients (76 MB) 15.6 us, 4.8 TB/s, and 3.9 us for the sum of the partials.
+// One row of 2560 takes 3.8 us, a launch and a few round trips to memory.
 constexpr int kNormMaxN = 32768;
 
 struct NormArgs {

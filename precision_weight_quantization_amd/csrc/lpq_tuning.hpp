@@ -167,8 +167,11 @@
 #ifndef LPQ_RQN_T
 #define LPQ_RQN_T LPQ_FLAT_THREADS
 #endif
-// MXFP4 codec (vectors per lane, workgroup size, load order): 128 threads of 4 vectors take 12.2 us
-// for 9728 x 2560 both ways, other shapes (1, 2 or 4 vectors, 128 to 512 threads) 12.2 to 13.9.
+// MXFP4 codec (vectors per lane, workgroup size, load order), each of 1, 2 or 4 vectors, 128, 256 or 512
+// threads and both load orders timed twice at 9728 x 2560 and 128 x 2560, us:
+//   quantize    4 vectors of 128 threads, one ahead: 11.9 and 2.8; the others 11.8 to 13.8 and 2.3 to 3.3
+//   dequantize  4 of 128, all at once: 12.3 and 2.4; the others 11.8 (4 of 256, all at once) to 14.3 and 2.3 to 3.5
+//   fake-quant  4 of 128, one ahead: 17.9 and 3.2; the others 17.4 (1 of 512) to 18.2 and 2.3 to 3.5
 #ifndef LPQ_MX4Q_U
 #define LPQ_MX4Q_U 4
 #endif
