@@ -31,40 +31,40 @@ def listed():
     return [
         # the tokens of a training batch in front of the experts' products; an expert's rows are
         # padded to whole blocks, as the weight gradient needs them
-        {"name": "dispatch 8192x8 of 128, fp8 2048", "op": "dispatch", "t": 8192, "k": 8, "groups": 128, "n": 2048, "align": 32,
+        {"name": "dispatch 8192x8 of 128 fp8 2048", "op": "dispatch", "t": 8192, "k": 8, "groups": 128, "n": 2048, "align": 32,
          "format": FP8, "drop": False},
         # one decoded token on a rank that holds half of the experts, 4-bit activations
-        {"name": "dispatch 1x8 of 64, fp4 2048", "op": "dispatch", "t": 1, "k": 8, "groups": 64, "n": 2048, "align": 1,
+        {"name": "dispatch 1x8 of 64 fp4 2048", "op": "dispatch", "t": 1, "k": 8, "groups": 64, "n": 2048, "align": 1,
          "format": FP4, "drop": True},
         # gate and up projections of a training batch or a long prompt, 8-bit operands
-        {"name": "experts fp8 8192x8 of 128, 1536x2048", "op": "experts", "t": 8192, "k": 8, "groups": 128, "n": 1536, "K": 2048,
+        {"name": "experts fp8 8192x8 of 128 1536x2048", "op": "experts", "t": 8192, "k": 8, "groups": 128, "n": 1536, "K": 2048,
          "align": 32, "a": FP8, "b": FP8, "out": "bf16"},
         # the down projection of a decoding batch: few rows an expert, 4-bit weights
-        {"name": "experts fp8 fp4 24x8 of 128, 2048x768", "op": "experts", "t": 24, "k": 8, "groups": 128, "n": 2048, "K": 768,
+        {"name": "experts fp8 fp4 24x8 of 128 2048x768", "op": "experts", "t": 24, "k": 8, "groups": 128, "n": 2048, "K": 768,
          "align": 1, "a": FP8, "b": FP4, "out": "bf16"},
         # a short prompt, sizes that fill no tile, 4-bit operands and an FP32 result
-        {"name": "experts fp4 701x6 of 60, 1021x1056", "op": "experts", "t": 701, "k": 6, "groups": 60, "n": 1021, "K": 1056,
+        {"name": "experts fp4 701x6 of 60 1021x1056", "op": "experts", "t": 701, "k": 6, "groups": 60, "n": 1021, "K": 1056,
          "align": 1, "a": FP4, "b": FP4, "out": "f32"},
         # the weight gradient of the gate and up projections over a training batch
-        {"name": "experts grad fp8 8192x8 of 128, 1536x2048", "op": "experts_grad", "t": 8192, "k": 8, "groups": 128, "n": 1536,
+        {"name": "experts grad fp8 8192x8 of 128 1536x2048", "op": "experts_grad", "t": 8192, "k": 8, "groups": 128, "n": 1536,
          "K": 2048, "a": FP8, "b": FP8, "out": "bf16"},
         # a small batch over many experts, some without a token; 4-bit operands, FP32 gradients
-        {"name": "experts grad fp4 157x4 of 96, 520x776", "op": "experts_grad", "t": 157, "k": 4, "groups": 96, "n": 520, "K": 776,
+        {"name": "experts grad fp4 157x4 of 96 520x776", "op": "experts_grad", "t": 157, "k": 4, "groups": 96, "n": 520, "K": 776,
          "a": FP4, "b": FP4, "out": "f32"},
         # the experts' outputs of a training batch back into the residual stream
-        {"name": "combine 8192x8, 2048", "op": "combine", "t": 8192, "k": 8, "groups": 128, "n": 2048, "align": 1,
+        {"name": "combine 8192x8 2048", "op": "combine", "t": 8192, "k": 8, "groups": 128, "n": 2048, "align": 1,
          "residual": True, "drop": False, "backward": False},
         # its backward pass on a rank that holds half of the experts: gradients of the outputs and weights
-        {"name": "combine grad 1237x6, 7168", "op": "combine", "t": 1237, "k": 6, "groups": 64, "n": 7168, "align": 32,
+        {"name": "combine grad 1237x6 7168", "op": "combine", "t": 1237, "k": 6, "groups": 64, "n": 7168, "align": 32,
          "residual": False, "drop": True, "backward": True},
         # prompts of a few requests, each with its own adapter, through a gate projection
-        {"name": "adapters 8192 of 8, 9728x2560 rank 64", "op": "adapters", "t": 8192, "groups": 8, "n": 9728, "K": 2560, "rank": 64,
+        {"name": "adapters 8192 of 8 9728x2560 rank 64", "op": "adapters", "t": 8192, "groups": 8, "n": 9728, "K": 2560, "rank": 64,
          "backward": False},
         # one decoding step of many requests, nearly every one with another adapter
-        {"name": "adapters 40 of 32, 4096x2560 rank 16", "op": "adapters", "t": 40, "groups": 32, "n": 4096, "K": 2560, "rank": 16,
+        {"name": "adapters 40 of 32 4096x2560 rank 16", "op": "adapters", "t": 40, "groups": 32, "n": 4096, "K": 2560, "rank": 16,
          "backward": False},
         # fine-tuning several adapters in one batch: gradients of the input and of both factors
-        {"name": "adapters grad 4099 of 4, 1024x2560 rank 24", "op": "adapters", "t": 4099, "groups": 4, "n": 1024, "K": 2560,
+        {"name": "adapters grad 4099 of 4 1024x2560 rank 24", "op": "adapters", "t": 4099, "groups": 4, "n": 1024, "K": 2560,
          "rank": 24, "backward": True},
     ]
 
