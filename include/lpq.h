@@ -561,6 +561,64 @@ lpq_status lpq_rmsnorm_backward(const uint16_t* dy, const uint16_t* h, const uin
 lpq_status lpq_mx_matmul(const uint8_t* a, const uint8_t* ae, int a_format, const uint8_t* b, const uint8_t* be, int b_format,
                          int64_t M, int64_t N, int64_t K, void* y, int y_type, void* stream);
 
+/* ======================================================================== */
+/* Layers whose rows go to different weights: a mixture of experts, or low-rank
+ * adapters of many requests.  A plan orders the rows by their weight ("group");
+ * all of it is made and read on the device, so that a step needs no copy to the
+ * host and can be captured.
+ *
+ * lpq_route_plan: ids [pairs] (id_bytes 4: int32, 8: int64) is the group of each
+ * pair; with k groups a token, pair p is slot p % k of token p / k.  An id outside
+ * [0, groups) has no row here (another rank's expert, a request without an adapter).
+ *   offsets [groups + 1]  group g has the rows offsets[g] to offsets[g + 1] - 1: its
+ *                         pairs in their order, then padding up to a multiple of
+ *                         `align` (1 to 1024; 32 where weight gradients follow, whose
+ *                         operands' blocks run along the rows)
+ *   rows [pairs]          the row of each pair, -1 without one
+ *   src [capacity]        the pair of each row, -1 for padding and behind the last group
+ * capacity: rows of the buffers, at least lpq_route_capacity(pairs, groups, align)
+ * = pairs + min(groups, pairs) * (align - 1), rounded up to a multiple of align: enough
+ * for every routing (0 for invalid arguments; LPQ_ERR_SHAPE).  1 to 1024 groups; pairs
+ * and capacity up to 2^30.  workspace: lpq_route_plan_workspace(pairs, groups) bytes
+ * (may be 0), 4-byte aligned, for this call alone while it runs.
+ *
+ * The calls below that read a plan keep inside their buffers whatever it holds, but
+ * their results are defined for what lpq_route_plan writes only. */
+int64_t lpq_route_capacity(int64_t pairs, int32_t groups, int32_t align);
+int64_t lpq_route_plan_workspace(int64_t pairs, int32_t groups);
+lpq_status lpq_route_plan(const void* ids, int id_bytes, int64_t pairs, int32_t groups, int32_t align, int32_t* offsets,
+                          int32_t* rows, int32_t* src, int64_t capacity, void* workspace, int64_t workspace_bytes, void* stream);
+
+/* The tokens in the plan's order: row rows[t, j] of the result is x[t], in BF16 (y) or
+ * quantized as lpq_quantize_mxfp8 / lpq_quantize_mxfp4 do it, bit for bit; rows
+ * without a pair are zeros (codes and scale bytes 0).  x: [tokens, N] BF16; rows:
+ * [tokens, k]; src: [capacity]; y: [capacity, N] BF16, q: [capacity, N], p:
+ * [capacity, N/2], e: [capacity, N/32].  N % 32 == 0; x, y, q and p 16-byte aligned; no
+ * output may overlap another array (LPQ_ERR_ARG).  The gradient of a gather is
+ * lpq_route_combine without weights. */
+lpq_status lpq_route_gather(const uint16_t* x, int64_t tokens, int64_t N, const int32_t* rows, int64_t k, const int32_t* src,
+                            int64_t capacity, uint16_t* y, void* stream);
+lpq_status lpq_route_gather_mxfp8(const uint16_t* x, int64_t tokens, int64_t N, const int32_t* rows, int64_t k, const int32_t* src,
+                                  int64_t capacity, uint8_t* q, uint8_t* e, void* stream);
+lpq_status lpq_route_gather_mxfp4(const uint16_t* x, int64_t tokens, int64_t N, const int32_t* rows, int64_t k, const int32_t* src,
+                                  int64_t capacity, uint8_t* p, uint8_t* e, void* stream);
+
+/* Back to the tokens' order:
+ *   out[t] = BF16(residual[t] + sum over j of weights[t, j] * y[rows[t, j]])
+ * FP32, in the order of j; a slot without a row adds nothing.  weights [tokens, k]
+ * FP32, NULL: ones; residual [tokens, N] BF16, NULL: none, and may be out itself.
+ * Backward, from dout [tokens, N]:
+ *   dy[rows[t, j]] = BF16(weights[t, j] * dout[t])   rows without a pair: zeros
+ *   dweights[t, j] = sum over n of dout[t, n] * y[rows[t, j], n]   FP32, in a fixed
+ *                    order; 0 for a slot without a row; NULL: not wanted (y is not read)
+ * The gradient of residual is dout.  Shapes and alignment as above; outputs overlap
+ * nothing else (LPQ_ERR_ARG). */
+lpq_status lpq_route_combine(const uint16_t* y, int64_t capacity, int64_t N, const int32_t* rows, int64_t tokens, int64_t k,
+                             const float* weights, const uint16_t* residual, uint16_t* out, void* stream);
+lpq_status lpq_route_combine_backward(const uint16_t* dout, const uint16_t* y, int64_t capacity, int64_t N, const int32_t* rows,
+                                      const int32_t* src, int64_t tokens, int64_t k, const float* weights, uint16_t* dy,
+                                      float* dweights, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

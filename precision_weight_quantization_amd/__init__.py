@@ -95,6 +95,14 @@ _SIG = {
     "lpq_rmsnorm_backward_workspace": (_i64, [_i64, _i64]),
     "lpq_rmsnorm_backward": (_int, [_vp, _vp, _vp, _vp, _vp, _i64, _i64, _vp, _vp, _int, _vp, _i64, _vp]),
     "lpq_mx_matmul": (_int, [_vp, _vp, _int, _vp, _vp, _int, _i64, _i64, _i64, _vp, _int, _vp]),
+    "lpq_route_capacity": (_i64, [_i64, _i32, _i32]),
+    "lpq_route_plan_workspace": (_i64, [_i64, _i32]),
+    "lpq_route_plan": (_int, [_vp, _int, _i64, _i32, _i32, _vp, _vp, _vp, _i64, _vp, _i64, _vp]),
+    "lpq_route_gather": (_int, [_vp, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _vp]),
+    "lpq_route_gather_mxfp8": (_int, [_vp, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp]),
+    "lpq_route_gather_mxfp4": (_int, [_vp, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp]),
+    "lpq_route_combine": (_int, [_vp, _i64, _i64, _vp, _i64, _i64, _vp, _vp, _vp, _vp]),
+    "lpq_route_combine_backward": (_int, [_vp, _vp, _i64, _i64, _vp, _vp, _i64, _i64, _vp, _vp, _vp, _vp]),
     "lpq_nvfp4_global_scale_reciprocal": (_int, [_vp, _i32, _vp, _vp]),
     "lpq_nvfp4_global_scale": (_int, [_vp, _i32, _vp, _vp]),
     "lpq_quantize_nvfp4_ex": (_int, [_vp, _i64, _i64, _vp, _int, _vp, _vp, _vp, _vp]),
@@ -998,3 +1006,21 @@ def lpq_requantize_fp8blk_nvfp4_grouped(table: RequantTable, group_amax, group_g
 def raw():
     """The ctypes handle of liblpq.so (for tests of the C ABI itself)."""
     return _L
+
+
+# --------------------------------------------------------------------------- routed layers
+
+# The calls of layers whose rows go to different weights (routed.py), found here under their C names.
+_ROUTED = ("lpq_route_capacity", "lpq_route_plan", "lpq_route_gather", "lpq_route_gather_mxfp8", "lpq_route_gather_mxfp4",
+           "lpq_route_combine", "lpq_route_combine_backward")
+
+
+def __getattr__(name):
+    if name in _ROUTED:
+        from . import routed
+        return getattr(routed, name)
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+
+
+def __dir__():
+    return sorted([*globals(), *_ROUTED])

@@ -57,6 +57,7 @@ using namespace lpq;
 #include "lpq_mx_transpose.hpp"
 #include "lpq_rmsnorm.hpp"
 #include "lpq_mx_matmul.hpp"
+#include "lpq_route.hpp"
 
 
 // ===========================================================================
@@ -1263,3 +1264,6 @@ lpq_status lpq_int4_qdq_grouped(const lpq_tensor* host, const lpq_tensor* dev, i
 }
 
 }  // extern "C"
+
+// The routed layers' calls, on the helpers above.
+#include "lpq_routed_calls.hpp"

@@ -1,0 +1,168 @@
+// Host side of the routed layers: argument checks and launches.
+//
+// Part of lpq_kernels.hip, which includes each part once, in this order: one
+// translation unit.
+#pragma once
+
+namespace {
+
+struct Range {
+    const void* p;
+    int64_t n;   // bytes; an absent array has none
+};
+inline Range range(const void* p, int64_t n) { return {p, p ? n : 0}; }
+
+// An output that shares a byte with an input or another output.
+template <int O, int I>
+bool any_overlap(const Range (&out)[O], const Range (&in)[I]) {
+    for (int i = 0; i < O; i++) {
+        for (const Range& r : in)
+            if (overlap(out[i].p, out[i].n, r.p, r.n)) return true;
+        for (int j = 0; j < i; j++)
+            if (overlap(out[i].p, out[i].n, out[j].p, out[j].n)) return true;
+    }
+    return false;
+}
+
+// Rows of a routed matrix are counted in 32 bits, pairs too.
+constexpr int64_t kRouteMaxRows = int64_t(1) << 30;
+
+int64_t route_capacity(int64_t pairs, int32_t groups, int32_t align) {
+    if (pairs <= 0 || pairs > kRouteMaxRows || groups <= 0 || groups > kRouteMaxGroups || align <= 0 || align > 1024) return 0;
+    const int64_t most = pairs + (pairs < groups ? pairs : groups) * (int64_t)(align - 1), c = ceil_div(most, align) * align;
+    return c <= kRouteMaxRows ? c : 0;
+}
+
+// Workgroups of a plan: runs of whole kPlanThreads pairs.
+int64_t plan_runs(int64_t pairs) {
+    if (pairs <= kPlanOne) return 1;
+    const int64_t run = ceil_div(ceil_div(pairs, kPlanThreads), kPlanMaxRuns) * kPlanThreads;
+    return ceil_div(pairs, run);
+}
+
+template <typename Id>
+lpq_status route_plan(PlanArgs A, hipStream_t s) {
+    const int64_t runs = plan_runs(A.pairs);
+    A.run = ceil_div(ceil_div(A.pairs, kPlanThreads), runs) * kPlanThreads;
+    if (runs == 1) A.counts = nullptr;
+    else {
+        hipLaunchKernelGGL(k_route_count<Id>, dim3((unsigned)runs), dim3(kPlanThreads), 0, s, A);
+        const lpq_status st = launched();
+        if (st != LPQ_OK) return st;
+    }
+    hipLaunchKernelGGL(k_route_place<Id>, dim3((unsigned)runs), dim3(kPlanThreads), 0, s, A);
+    return launched();
+}
+
+// Shape of tokens with k rows each in a routed matrix of `capacity` rows, N elements a row.
+lpq_status route_shape(int64_t tokens, int64_t k, int64_t capacity, int64_t N) {
+    if (tokens <= 0 || k <= 0 || capacity <= 0 || N <= 0 || N % 32) return LPQ_ERR_SHAPE;
+    if (N > kRouteMaxRows || capacity > kRouteMaxRows || tokens > kRouteMaxRows / k) return LPQ_ERR_SHAPE;
+    if (tokens > (int64_t(1) << 40) / N || capacity > (int64_t(1) << 40) / N) return LPQ_ERR_SHAPE;
+    return LPQ_OK;
+}
+
+int64_t pad_groups(int64_t capacity, int threads) { return ceil_div(capacity, threads); }   // a wave to 64 rows
+
+template <int FORMAT>
+lpq_status route_gather(const uint16_t* x, int64_t tokens, int64_t N, const int32_t* rows, int64_t k, const int32_t* src,
+                        int64_t capacity, void* q, uint8_t* e, void* stream) {
+    const lpq_status st = route_shape(tokens, k, capacity, N);
+    if (st != LPQ_OK) return st;
+    const int64_t pad = pad_groups(capacity, kRouteThreads), blocks = pad + ceil_div(tokens * (N / 8), kRouteThreads);
+    if (blocks > max_groups(kRouteThreads)) return LPQ_ERR_SHAPE;
+    if (!x || !rows || !src || !q || (FORMAT != ROW_BF16 && !e)) return LPQ_ERR_NULL;
+    if (!aligned(x, 16) || !aligned(q, 16) || !aligned(rows, 4) || !aligned(src, 4)) return LPQ_ERR_ALIGN;
+    const int64_t size = FORMAT == ROW_BF16 ? 2 * capacity * N : FORMAT == ROW_FP8 ? capacity * N : capacity * N / 2;
+    if (any_overlap({range(q, size), range(e, capacity * N / 32)},
+                    {range(x, 2 * tokens * N), range(rows, 4 * tokens * k), range(src, 4 * capacity)}))
+        return LPQ_ERR_ARG;
+    const GatherArgs A{x, rows, src, static_cast<uint8_t*>(q), e, tokens, capacity, (int32_t)k, (int32_t)N, (int32_t)pad};
+    hipLaunchKernelGGL(k_route_gather<FORMAT>, dim3((unsigned)blocks), dim3(kRouteThreads), 0, (hipStream_t)stream, A);
+    return launched();
+}
+
+}  // namespace
+
+extern "C" {
+
+int64_t lpq_route_capacity(int64_t pairs, int32_t groups, int32_t align) { return route_capacity(pairs, groups, align); }
+
+int64_t lpq_route_plan_workspace(int64_t pairs, int32_t groups) {
+    if (route_capacity(pairs, groups, 1) == 0) return 0;
+    const int64_t runs = plan_runs(pairs);
+    return runs == 1 ? 0 : 4 * runs * groups;
+}
+
+lpq_status lpq_route_plan(const void* ids, int id_bytes, int64_t pairs, int32_t groups, int32_t align, int32_t* offsets,
+                          int32_t* rows, int32_t* src, int64_t capacity, void* workspace, int64_t workspace_bytes, void* stream) {
+    const int64_t least = route_capacity(pairs, groups, align), need = lpq_route_plan_workspace(pairs, groups);
+    if (least == 0 || capacity < least || capacity > kRouteMaxRows) return LPQ_ERR_SHAPE;
+    if (!ids || !offsets || !rows || !src || (need && !workspace)) return LPQ_ERR_NULL;
+    if ((id_bytes != 4 && id_bytes != 8) || workspace_bytes < need) return LPQ_ERR_ARG;
+    if (!aligned(ids, id_bytes) || !aligned(offsets, 4) || !aligned(rows, 4) || !aligned(src, 4) || !aligned(workspace, 4))
+        return LPQ_ERR_ALIGN;
+    if (any_overlap({range(offsets, 4 * (groups + 1)), range(rows, 4 * pairs), range(src, 4 * capacity), range(workspace, need)},
+                    {range(ids, id_bytes * pairs)}))
+        return LPQ_ERR_ARG;
+    const PlanArgs A{ids, pairs, 0, groups, align, offsets, rows, src, capacity, static_cast<int32_t*>(workspace)};
+    return id_bytes == 4 ? route_plan<int32_t>(A, (hipStream_t)stream) : route_plan<int64_t>(A, (hipStream_t)stream);
+}
+
+lpq_status lpq_route_gather(const uint16_t* x, int64_t tokens, int64_t N, const int32_t* rows, int64_t k, const int32_t* src,
+                            int64_t capacity, uint16_t* y, void* stream) {
+    return route_gather<ROW_BF16>(x, tokens, N, rows, k, src, capacity, y, nullptr, stream);
+}
+
+lpq_status lpq_route_gather_mxfp8(const uint16_t* x, int64_t tokens, int64_t N, const int32_t* rows, int64_t k, const int32_t* src,
+                                  int64_t capacity, uint8_t* q, uint8_t* e, void* stream) {
+    return route_gather<ROW_FP8>(x, tokens, N, rows, k, src, capacity, q, e, stream);
+}
+
+lpq_status lpq_route_gather_mxfp4(const uint16_t* x, int64_t tokens, int64_t N, const int32_t* rows, int64_t k, const int32_t* src,
+                                  int64_t capacity, uint8_t* p, uint8_t* e, void* stream) {
+    return route_gather<ROW_FP4>(x, tokens, N, rows, k, src, capacity, p, e, stream);
+}
+
+lpq_status lpq_route_combine(const uint16_t* y, int64_t capacity, int64_t N, const int32_t* rows, int64_t tokens, int64_t k,
+                             const float* weights, const uint16_t* residual, uint16_t* out, void* stream) {
+    const lpq_status st = route_shape(tokens, k, capacity, N);
+    if (st != LPQ_OK) return st;
+    const int64_t blocks = ceil_div(tokens * (N / 8), kRouteThreads);
+    if (blocks > max_groups(kRouteThreads)) return LPQ_ERR_SHAPE;
+    if (!y || !rows || !out) return LPQ_ERR_NULL;
+    if (!aligned(y, 16) || !aligned(residual, 16) || !aligned(out, 16) || !aligned(rows, 4) || !aligned(weights, 4)) return LPQ_ERR_ALIGN;
+    if (any_overlap({range(out, 2 * tokens * N)},   // out may be the residual itself: a thread reads what it writes first
+                    {range(y, 2 * capacity * N), range(rows, 4 * tokens * k), range(weights, 4 * tokens * k),
+                     range(residual == out ? nullptr : residual, 2 * tokens * N)}))
+        return LPQ_ERR_ARG;
+    const CombineArgs A{y, rows, weights, residual, out, tokens, capacity, (int32_t)k, (int32_t)N};
+    hipLaunchKernelGGL(k_route_combine, dim3((unsigned)blocks), dim3(kRouteThreads), 0, (hipStream_t)stream, A);
+    return launched();
+}
+
+lpq_status lpq_route_combine_backward(const uint16_t* dout, const uint16_t* y, int64_t capacity, int64_t N, const int32_t* rows,
+                                      const int32_t* src, int64_t tokens, int64_t k, const float* weights, uint16_t* dy,
+                                      float* dweights, void* stream) {
+    const lpq_status st = route_shape(tokens, k, capacity, N);
+    if (st != LPQ_OK) return st;
+    const bool wide = N > 512;   // one wave to a row of up to 64 vectors
+    const int threads = wide ? 256 : 64;
+    const int64_t pad = pad_groups(capacity, threads), blocks = pad + tokens;
+    if (blocks > max_groups(threads)) return LPQ_ERR_SHAPE;
+    if (!dout || !rows || !src || !dy || (dweights && !y)) return LPQ_ERR_NULL;
+    if (!aligned(dout, 16) || !aligned(y, 16) || !aligned(dy, 16) || !aligned(rows, 4) || !aligned(src, 4) || !aligned(weights, 4) ||
+        !aligned(dweights, 4))
+        return LPQ_ERR_ALIGN;
+    if (any_overlap({range(dy, 2 * capacity * N), range(dweights, 4 * tokens * k)},
+                    {range(dout, 2 * tokens * N), range(dweights ? y : nullptr, 2 * capacity * N), range(rows, 4 * tokens * k),
+                     range(src, 4 * capacity), range(weights, 4 * tokens * k)}))
+        return LPQ_ERR_ARG;
+    const CombineGradArgs A{dout, dweights ? y : nullptr, rows, src, weights, dy, dweights, tokens, capacity, (int32_t)k, (int32_t)N,
+                            (int32_t)pad};
+    if (wide) hipLaunchKernelGGL(k_route_combine_grad<256>, dim3((unsigned)blocks), dim3(256), 0, (hipStream_t)stream, A);
+    else hipLaunchKernelGGL(k_route_combine_grad<64>, dim3((unsigned)blocks), dim3(64), 0, (hipStream_t)stream, A);
+    return launched();
+}
+
+}  // extern "C"

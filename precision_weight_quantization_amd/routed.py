@@ -1,0 +1,153 @@
+"""Binding of the routed layers' calls: rows that go to different weights.
+
+A plan orders tokens by their group (an expert, an adapter) on the device; the gather,
+the products, the combination and the adapters read it there.  The functions are found in
+the package under the same names, and follow its manner: device tensors in, outputs
+allocated when not passed (on ``stream`` if one is given), launches on the device of the
+data.  Indexes are ``torch.int32``.
+"""
+from __future__ import annotations
+
+import torch
+
+import precision_weight_quantization_amd as _p
+from precision_weight_quantization_amd import _arg, _bf16_in, _empty, _launch, _on, _outs, _ptr
+
+_I32 = (torch.int32,)
+
+
+# --------------------------------------------------------------------------- plan
+
+def lpq_route_capacity(pairs: int, groups: int, align: int = 1) -> int:
+    """Rows that hold every routing of so many pairs, each group's rows padded to ``align``."""
+    n = _p._L.lpq_route_capacity(pairs, groups, align)
+    if n == 0:
+        raise ValueError(f"no plan of {pairs} pairs over {groups} groups with rows padded to {align}: 1 to 1024 groups, "
+                         "1 to 1024 rows, up to 2^30 rows in all")
+    return n
+
+
+def lpq_route_plan(ids, groups, align=1, offsets=None, rows=None, src=None, workspace=None, stream=None):
+    """The rows of each group: ids (int32 or int64, [tokens, k] or [tokens]; outside [0, groups): no row) ->
+    (offsets [groups+1], rows like ids (-1: none), src [capacity], the pair of each row (-1: padding)), all int32.
+    A src passed in sets the capacity, at least ``lpq_route_capacity(ids.numel(), groups, align)`` rows."""
+    _arg(ids, "ids", dtypes=(torch.int32, torch.int64))
+    pairs = ids.numel()
+    capacity = lpq_route_capacity(pairs, groups, align)
+    need = _p._L.lpq_route_plan_workspace(pairs, groups)
+    if src is not None:
+        _arg(src, "src", ids, 4 * capacity, dtypes=_I32)
+        capacity = src.numel()
+    if workspace is not None:
+        _arg(workspace, "workspace", ids, need)
+    for t, name in ((offsets, "offsets"), (rows, "rows")):
+        if t is not None:
+            _arg(t, name, ids, dtypes=_I32)
+    with _on(stream, ids):
+        offsets, rows, src = _outs(ids, (offsets, "offsets", 4 * (groups + 1), (groups + 1,), torch.int32, 4),
+                                   (rows, "rows", 4 * pairs, ids.shape, torch.int32, 4),
+                                   (src, "src", 4 * capacity, (capacity,), torch.int32, 4))
+        if need and workspace is None:
+            workspace = _empty((need,), torch.uint8, ids)
+    _launch(_p._L.lpq_route_plan, "lpq_route_plan", ids, stream, ids.data_ptr(), ids.element_size(), pairs, groups, align,
+            offsets.data_ptr(), rows.data_ptr(), src.data_ptr(), capacity, _ptr(workspace),
+            0 if workspace is None else workspace.numel() * workspace.element_size())
+    return offsets, rows, src
+
+
+def _tokens(rows, like, tokens=None):
+    """(tokens, k) of the rows of a plan, [tokens, k] or [tokens]."""
+    _arg(rows, "rows", like, dtypes=_I32)
+    if rows.dim() not in (1, 2):
+        raise ValueError(f"rows must be [tokens, k] or [tokens], got shape {tuple(rows.shape)}")
+    if tokens is not None and rows.shape[0] != tokens:
+        raise ValueError(f"rows is of {rows.shape[0]} tokens, the call's data of {tokens}")
+    return rows.shape[0], rows.shape[1] if rows.dim() == 2 else 1
+
+
+# --------------------------------------------------------------------------- gather
+
+def lpq_route_gather(x, rows, src, y=None, stream=None):
+    """x [tokens,N] BF16 (N % 32 == 0) in a plan's order: [src.numel(), N] BF16, zeros in rows without a token."""
+    x = _bf16_in(x, "x")
+    T, N = x.shape
+    _, k = _tokens(rows, x, T)
+    R = _arg(src, "src", x, dtypes=_I32).numel()
+    with _on(stream, x):
+        y, = _outs(x, (y, "y", 2 * R * N, (R, N), torch.bfloat16, 2))
+    _launch(_p._L.lpq_route_gather, "lpq_route_gather", x, stream, x.data_ptr(), T, N, rows.data_ptr(), k, src.data_ptr(), R,
+            y.data_ptr())
+    return y
+
+
+def lpq_route_gather_mxfp8(x, rows, src, q=None, e=None, stream=None):
+    """As lpq_route_gather, quantized: (codes [R,N] float8_e4m3fn, UE8M0 bytes [R,N/32] uint8)."""
+    x = _bf16_in(x, "x")
+    T, N = x.shape
+    _, k = _tokens(rows, x, T)
+    R = _arg(src, "src", x, dtypes=_I32).numel()
+    with _on(stream, x):
+        q, e = _outs(x, (q, "q", R * N, (R, N), torch.float8_e4m3fn, 1),
+                     (e, "e", R * (N // 32), (R, max(N // 32, 1)), torch.uint8, 1))
+    _launch(_p._L.lpq_route_gather_mxfp8, "lpq_route_gather_mxfp8", x, stream, x.data_ptr(), T, N, rows.data_ptr(), k,
+            src.data_ptr(), R, q.data_ptr(), e.data_ptr())
+    return q, e
+
+
+def lpq_route_gather_mxfp4(x, rows, src, p=None, e=None, stream=None):
+    """As lpq_route_gather, quantized: (packed E2M1 codes [R,N/2] uint8, UE8M0 bytes [R,N/32] uint8)."""
+    x = _bf16_in(x, "x")
+    T, N = x.shape
+    _, k = _tokens(rows, x, T)
+    R = _arg(src, "src", x, dtypes=_I32).numel()
+    with _on(stream, x):
+        p, e = _outs(x, (p, "p", R * (N // 2), (R, max(N // 2, 1)), torch.uint8, 1),
+                     (e, "e", R * (N // 32), (R, max(N // 32, 1)), torch.uint8, 1))
+    _launch(_p._L.lpq_route_gather_mxfp4, "lpq_route_gather_mxfp4", x, stream, x.data_ptr(), T, N, rows.data_ptr(), k,
+            src.data_ptr(), R, p.data_ptr(), e.data_ptr())
+    return p, e
+
+
+# --------------------------------------------------------------------------- combination
+
+def lpq_route_combine(y, rows, weights=None, residual=None, out=None, stream=None):
+    """out [tokens,N] = BF16(residual + sum over j of weights[:, j] * y[rows[:, j]]): y [R,N] BF16, weights like rows
+    FP32 (None: ones, the gradient of a gather), residual [tokens,N] BF16 or None (``out`` may be it)."""
+    y = _bf16_in(y, "y")
+    R, N = y.shape
+    T, k = _tokens(rows, y)
+    if weights is not None:
+        _arg(weights, "weights", y, 4 * T * k, dtypes=(torch.float32,))
+    if residual is not None:
+        _arg(residual, "residual", y, 2 * T * N, dtypes=_p._BF16)
+    with _on(stream, y):
+        out, = _outs(y, (out, "out", 2 * T * N, (T, N), torch.bfloat16, 2))
+    _launch(_p._L.lpq_route_combine, "lpq_route_combine", y, stream, y.data_ptr(), R, N, rows.data_ptr(), T, k, _ptr(weights),
+            _ptr(residual), out.data_ptr())
+    return out
+
+
+def lpq_route_combine_backward(dout, rows, src, weights=None, y=None, dy=None, dweights=None, want_dweights=True, stream=None):
+    """Gradients of lpq_route_combine from dout [tokens,N] BF16: (dy [R,N] BF16, zeros in rows without a token;
+    dweights like rows FP32, or None with ``want_dweights`` False, which needs no y)."""
+    dout = _bf16_in(dout, "dout")
+    T, N = dout.shape
+    _, k = _tokens(rows, dout, T)
+    R = _arg(src, "src", dout, dtypes=_I32).numel()
+    if want_dweights:
+        if y is None:
+            raise ValueError("the gradient of the weights needs y")
+        _arg(y, "y", dout, 2 * R * N, dtypes=_p._BF16)
+    elif dweights is not None:
+        raise ValueError("dweights was passed in, and want_dweights is False")
+    if weights is not None:
+        _arg(weights, "weights", dout, 4 * T * k, dtypes=(torch.float32,))
+    specs = [(dy, "dy", 2 * R * N, (R, N), torch.bfloat16, 2)]
+    if want_dweights:
+        specs.append((dweights, "dweights", 4 * T * k, rows.shape, torch.float32, 4))
+    with _on(stream, dout):
+        dy, dweights = (_outs(dout, *specs) + [None])[:2]
+    _launch(_p._L.lpq_route_combine_backward, "lpq_route_combine_backward", dout, stream, dout.data_ptr(),
+            _ptr(y) if want_dweights else 0, R, N, rows.data_ptr(), src.data_ptr(), T, k, _ptr(weights), dy.data_ptr(),
+            _ptr(dweights))
+    return dy, dweights
