@@ -619,6 +619,29 @@ lpq_status lpq_route_combine_backward(const uint16_t* dout, const uint16_t* y, i
                                       const int32_t* src, int64_t tokens, int64_t k, const float* weights, uint16_t* dy,
                                       float* dweights, void* stream);
 
+/* Products of microscaled matrices grouped by a plan, with the operands, formats, sums
+ * and result types of lpq_mx_matmul (FP32 for two MXFP4 operands only):
+ *   lpq_mx_matmul_routed      y[r] = a[r] b[g]^T for the rows r of each group g: a
+ *       [capacity, K], b [groups, N, K] (the groups' weights end to end), y [capacity,
+ *       N].  Padding rows are computed like the others; y's rows of no group are left
+ *       as they were.  A layer's forward product, and dx from dy with the transposed
+ *       weights.  K % 32 == 0.
+ *   lpq_mx_matmul_routed_dw   y[g] = the sum over the rows r of group g of a[:, r]
+ *       b[:, r]^T: a [M, capacity], b [N, capacity] as lpq_quantize_mxfp8_transposed
+ *       / lpq_quantize_mxfp4_transposed make them of gathered rows, y [groups, M, N]; a
+ *       group without rows gets zeros.  The weight gradients.  capacity % 32 == 0, and
+ *       a plan with an align that is a multiple of 32: blocks must not hold rows of
+ *       two groups (offsets are rounded down to whole blocks).
+ * offsets [groups + 1] is read on the device.  No array above 2^40 elements; y overlaps no
+ * other array (LPQ_ERR_ARG).  The order of a row's sums depends on the formats and on
+ * capacity, groups, N and K (M) only: a call's result does not vary. */
+lpq_status lpq_mx_matmul_routed(const uint8_t* a, const uint8_t* ae, int a_format, const uint8_t* b, const uint8_t* be, int b_format,
+                                const int32_t* offsets, int32_t groups, int64_t capacity, int64_t N, int64_t K, void* y, int y_type,
+                                void* stream);
+lpq_status lpq_mx_matmul_routed_dw(const uint8_t* a, const uint8_t* ae, int a_format, const uint8_t* b, const uint8_t* be,
+                                   int b_format, const int32_t* offsets, int32_t groups, int64_t M, int64_t N, int64_t capacity,
+                                   void* y, int y_type, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

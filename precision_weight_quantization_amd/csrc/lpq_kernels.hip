@@ -56,8 +56,9 @@ using namespace lpq;
 #include "lpq_requant.hpp"
 #include "lpq_mx_transpose.hpp"
 #include "lpq_rmsnorm.hpp"
-#include "lpq_mx_matmul.hpp"
 #include "lpq_route.hpp"
+#include "lpq_mx_matmul.hpp"
+#include "lpq_mx_routed.hpp"
 
 
 // ===========================================================================

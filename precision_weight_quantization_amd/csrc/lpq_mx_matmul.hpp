@@ -229,9 +229,14 @@ __device__ __forceinline__ void static_for(F&& f) {
     }
 }
 
-// N >= TN, M >= TM, at least two stages.
-template <bool FP4B, bool FP4A, int TN, int TM, int WN, int WM>
-__global__ __launch_bounds__(64 * WN * WM, 2) void k_mx_matmul_tile(MatmulArgs A, int tiles_n, int tiles_m) {
+// What the tiles are of: one product; products of runs of a's rows, each with its own
+// b (ragged m); or products over runs of the contraction, each with its own y (ragged k).
+enum TileMode { DENSE, ROUTED_ROWS, ROUTED_K };
+
+// N >= TN, M >= TM; DENSE and ROUTED_ROWS: at least two stages.  ROUTED_ROWS: b [groups, N, K], y's
+// rows of no group stay as they are.  ROUTED_K: operands [., K] of all groups, y [groups, M, N].
+template <bool FP4B, bool FP4A, int TN, int TM, int WN, int WM, TileMode MODE>
+__device__ __forceinline__ void mx_matmul_tiles(const MatmulArgs& A, int tiles_n, int tiles_m, const Routing& routing) {
     constexpr int T = 64 * WN * WM, KS = stage_steps<FP4B, FP4A>(), BK = 128 * KS;
     constexpr int PB = Stage<FP4B>::template pitch<KS>(), PA = Stage<FP4A>::template pitch<KS>();
     constexpr int CB = PB / 16, CA = PA / 16;                  // 16-byte pieces of a row
@@ -254,10 +259,19 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void k_mx_matmul_tile(MatmulArgs A
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wn = wave % WN, wm = wave / WN;
     const int pitch_b = row_bytes<FP4B>(A.K), pitch_a = row_bytes<FP4A>(A.K), blocks = A.K / 32;
-    const int full = A.K / BK, steps = (A.K + BK - 1) / BK;    // stages of a tile; the last one may pass K
+    const int dense_full = A.K / BK, dense_steps = (A.K + BK - 1) / BK;    // stages of a tile; the last one may pass K
+    // of a tile whose contraction has k elements: a group without rows has one stage of zeros
+    auto full_of = [&](int k) { return MODE == ROUTED_K ? k / BK : dense_full; };
+    auto steps_of = [&](int k) { return MODE == ROUTED_K ? max((k + BK - 1) / BK, 1) : dense_steps; };
 
     // this workgroup's tiles: every slots-th of its XCD's run
-    const int total = tiles_n * tiles_m, xcd = blockIdx.x % kXcds, each = total / kXcds, more = total % kXcds;
+    RouteMap map;
+    if constexpr (MODE == ROUTED_ROWS) {
+        map.open<TM>(routing);
+        tiles_m = map.total;
+    }
+    const int each_group = tiles_n * tiles_m;
+    const int total = MODE == ROUTED_K ? each_group * routing.groups : each_group, xcd = blockIdx.x % kXcds, each = total / kXcds, more = total % kXcds;
     const int run = xcd * each + min(xcd, more), run_end = run + each + (xcd < more);
     const int slots = ((int)gridDim.x - xcd + kXcds - 1) / kXcds;
 
@@ -269,41 +283,70 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void k_mx_matmul_tile(MatmulArgs A
 
     // The last tile of a row or column ends with the matrix: it repeats some of its neighbour's
     // results.
-    auto origin = [&](int tile, int64_t& n0, int64_t& m0) {
+    // A routed tile of rows that passes the buffer's end begins earlier; it stores its group's rows only.
+    struct Tile {
+        int64_t n0, m0;
+        int group;
+        int first, last;   // rows to store (ROUTED_ROWS)
+        int k0, k;         // the contraction's part (ROUTED_K)
+    };
+    auto tile_of = [&](int tile) {
+        Tile t{};
         int n, m;
+        if constexpr (MODE == ROUTED_K) {
+            t.group = tile / each_group;
+            tile -= t.group * each_group;
+            const RouteRun run = route_run(routing, t.group);
+            t.k = run.last / 32 * 32 - run.first / 32 * 32;   // whole blocks: a plan with align 32 has no others
+            t.k0 = min(run.first / 32 * 32, A.K - 32);
+        }
         tile_at(tile, tiles_n, tiles_m, n, m);
-        n0 = min((int64_t)n * TN, (int64_t)A.N - TN);
-        m0 = min((int64_t)m * TM, (int64_t)A.M - TM);
+        t.n0 = min((int64_t)n * TN, (int64_t)A.N - TN);
+        if constexpr (MODE == ROUTED_ROWS) {
+            const RouteTile r = map.find<TM>(routing, m);
+            t.group = r.group;
+            t.first = r.first;
+            t.last = r.last;
+            t.m0 = min(r.first, A.M - TM);
+        } else {
+            t.m0 = min((int64_t)m * TM, (int64_t)A.M - TM);
+        }
+        return t;
     };
     // the tile being loaded, its rows in memory, its next stage to load
     const int first_tile = run + blockIdx.x / kXcds;
     int load_tile = first_tile, load_step = 0;
+    int load_k = A.K;   // its contraction
     const uint8_t *gb = nullptr, *ga = nullptr, *gs[SR] = {};
     uint32_t off_s[SR];
 #pragma unroll
     for (int i = 0; i < SR; i++)
         off_s[i] = (uint32_t)(i * T / 64 + wave < kChunksB ? lane : min(lane, kRowsA - 1)) * blocks;
     auto open_tile = [&]() {
-        int64_t n0, m0;
-        origin(load_tile, n0, m0);
-        gb = A.b + n0 * pitch_b;
-        ga = A.a + m0 * pitch_a;
+        const Tile t = tile_of(load_tile);
+        int64_t n0 = t.n0, m0 = t.m0;
+        if constexpr (MODE == ROUTED_ROWS) n0 += (int64_t)t.group * A.N;
+        if constexpr (MODE == ROUTED_K) load_k = t.k;
+        gb = A.b + n0 * pitch_b + row_bytes<FP4B>(t.k0);
+        ga = A.a + m0 * pitch_a + row_bytes<FP4A>(t.k0);
 #pragma unroll
         for (int i = 0; i < SR; i++) {
             const int chunk = i * T / 64 + wave;
-            gs[i] = chunk < kChunksB ? A.be + (n0 + chunk * 64) * blocks : A.ae + (m0 + (chunk - kChunksB) * kRowsA) * blocks;
+            gs[i] = (chunk < kChunksB ? A.be + (n0 + chunk * 64) * blocks : A.ae + (m0 + (chunk - kChunksB) * kRowsA) * blocks) + t.k0 / 32;
         }
     };
     // Scale bytes come 16 to a row, enough for kGroup stages: a row's bytes lie far from
     // the next row's, and reading 4 at each stage asks for the same lines again (measured:
     // 20 us of 233 at 8192 x 9728 x 2560).  The last group is the last 16 bytes of the row,
     // so that a group is one load (a row of fewer has one group, read byte by byte).
-    auto group_start = [&](int group) { return max(min(group * 16, blocks - 16), 0); };
+    auto blocks_of = [&](int k) { return MODE == ROUTED_K ? k / 32 : blocks; };
+    auto group_start = [&](int group, int k) { return max(min(group * 16, blocks_of(k) - 16), 0); };
     v4u sc[SR];
     auto load_scales = [&](int group) {
+        const int blocks = blocks_of(load_k);
         if (blocks >= 16) {
 #pragma unroll
-            for (int i = 0; i < SR; i++) __builtin_memcpy(&sc[i], gs[i] + group_start(group) + off_s[i], 16);
+            for (int i = 0; i < SR; i++) __builtin_memcpy(&sc[i], gs[i] + group_start(group, load_k) + off_s[i], 16);
         } else {
 #pragma unroll
             for (int i = 0; i < SR; i++) {
@@ -339,33 +382,38 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void k_mx_matmul_tile(MatmulArgs A
             }
         }
     };
-    auto last_piece = [&](int step, int elems) { return min(A.K - step * BK, BK) / elems - 1; };
+    auto last_piece = [&](int k, int step, int elems) { return min((MODE == ROUTED_K ? k : A.K) - step * BK, BK) / elems - 1; };
+    // of a load: a stage of zeros loads its rows' first piece
+    auto last_load = [&](int step, int elems) {
+        const int p = last_piece(load_k, step, elems);
+        return MODE == ROUTED_K ? max(p, 0) : p;
+    };
     // the next stage of the tile being loaded, into buffer `buf`, and its scale group if it opens one
     auto load_stage = [&](int buf) {
         const int k0 = load_step * BK;
         const uint8_t* pb = gb + row_bytes<FP4B>(k0);
         const uint8_t* pa = ga + row_bytes<FP4A>(k0);
         const uint32_t to = lds0 + buf * kNextCodes + wave * 1024;
-        const uint32_t ob = off_b - max(src_b - last_piece(load_step, Stage<FP4B>::kElems), 0) * 16;
-        const uint32_t oa = off_a - max(src_a - last_piece(load_step, Stage<FP4A>::kElems), 0) * 16;
+        const uint32_t ob = off_b - max(src_b - last_load(load_step, Stage<FP4B>::kElems), 0) * 16;
+        const uint32_t oa = off_a - max(src_a - last_load(load_step, Stage<FP4A>::kElems), 0) * 16;
 #pragma unroll
         for (int i = 0; i < LB; i++) load_to_lds(pb + (int64_t)i * (T / CB) * pitch_b, ob, to + i * T * 16);
 #pragma unroll
         for (int i = 0; i < LA; i++) load_to_lds(pa + (int64_t)i * (T / CA) * pitch_a, oa, to + TN * PB + i * T * 16);
         if (load_step % kGroup == 0) load_scales(load_step / kGroup);
-        if (++load_step == steps) {
+        if (++load_step == steps_of(load_k)) {
             load_step = 0;
             load_tile += slots;
             if (load_tile < run_end) open_tile();
         }
     };
-    // the pieces of stage `step` that are past K, each lane its own
-    auto zero_tail = [&](int step, int buf) {
+    // the pieces of stage `step` that are past k, each lane its own
+    auto zero_tail = [&](int k, int step, int buf) {
         uint8_t* at = lds + buf * kNextCodes + tid * 16;
-        if (src_b > last_piece(step, Stage<FP4B>::kElems))
+        if (src_b > last_piece(k, step, Stage<FP4B>::kElems))
 #pragma unroll
             for (int i = 0; i < LB; i++) *reinterpret_cast<v4u*>(at + i * T * 16) = v4u{};
-        if (src_a > last_piece(step, Stage<FP4A>::kElems))
+        if (src_a > last_piece(k, step, Stage<FP4A>::kElems))
 #pragma unroll
             for (int i = 0; i < LA; i++) *reinterpret_cast<v4u*>(at + TN * PB + i * T * 16) = v4u{};
     };
@@ -378,8 +426,9 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void k_mx_matmul_tile(MatmulArgs A
     uint32_t a0 = TN * PB + row_a * PA + (g ^ swz_a) * 16, a1 = TN * PB + row_a * PA + ((4 + g) ^ swz_a) * 16;
     uint32_t sb[KS], sa[KS];
     int parity = 0;   // of the current scale group
-    auto scales_of = [&](int step) {   // blocks past K take the byte of the last one (their codes are zeros)
-        const int at = step * 4 * KS, start = group_start(step / kGroup), last = blocks - 1 - start;
+    auto scales_of = [&](int k, int step) {   // blocks past k take the byte of the last one (their codes are zeros)
+        const int at = step * 4 * KS, start = group_start(step / kGroup, k);
+        const int last = MODE == ROUTED_K ? max(blocks_of(k) - 1 - start, 0) : blocks - 1 - start;
         const uint32_t to = kScales0 + parity * kScales + r * 4;
 #pragma unroll
         for (int x = 0; x < KS; x++) {
@@ -448,13 +497,19 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void k_mx_matmul_tile(MatmulArgs A
         });
     };
 
+    if constexpr (MODE != DENSE)
+        if (first_tile >= run_end) return;   // uniform over the workgroup: the grid is for the most tiles there may be
     open_tile();
+    int k = A.K, next_k = A.K;   // of the tile that is computed, and of the next one
+    if constexpr (MODE == ROUTED_K) k = load_k;
     load_stage(0);
     put_scales(0);
     lds_arrived();
+    if constexpr (MODE == ROUTED_K)
+        if (full_of(k) == 0) zero_tail(k, 0, 0);
     __syncthreads();
     load_stage(1);
-    scales_of(0);
+    scales_of(k, 0);
 #pragma unroll
     for (int j = 0; j < FM; j++) fa[j] = frag_a(j, 0);
     auto first_rows = [&]() {
@@ -467,6 +522,9 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void k_mx_matmul_tile(MatmulArgs A
     int buf = 0;
     for (int tile = first_tile; tile < run_end; tile += slots) {
         clear();
+        const int steps = steps_of(k);
+        if constexpr (MODE == ROUTED_K)
+            if (tile + slots < run_end) next_k = tile_of(tile + slots).k;
         for (int s = 0; s < steps; s++) {
             static_for<FN * KS - 1>([&](auto at) {
                 constexpr int x = decltype(at)::value, i = x % FN, ks = x / FN;
@@ -491,13 +549,14 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void k_mx_matmul_tile(MatmulArgs A
             const int next_step = s + 1 == steps ? 0 : s + 1;
             if (next_step % kGroup == 0) put_scales(parity ^ 1);
             lds_arrived();
-            if (next_step == full) zero_tail(next_step, buf ^ 1);
+            const int step_k = MODE == ROUTED_K && next_step == 0 ? next_k : k;   // of the stage that comes
+            if (next_step == full_of(step_k)) zero_tail(step_k, next_step, buf ^ 1);
             __syncthreads();
             if (load_tile < run_end) load_stage(buf);   // of this tile or of the next
             buf ^= 1;
             parity ^= next_step % kGroup == 0;
             b0 ^= kNextCodes, b1 ^= kNextCodes, a0 ^= kNextCodes, a1 ^= kNextCodes;
-            scales_of(next_step);
+            scales_of(step_k, next_step);
             Frag<FP4B> next[kAhead];
 #pragma unroll
             for (int i = 0; i < kAhead; i++) next[i] = frag_b(i, 0);
@@ -508,9 +567,17 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void k_mx_matmul_tile(MatmulArgs A
             for (int i = 0; i < kAhead; i++) fb[i] = next[i];
             pin();
         }
-        int64_t n0, m0;
-        origin(tile, n0, m0);
-        n0 += wn * FN * 16, m0 += wm * FM * 16;
+        const Tile at = tile_of(tile);
+        if constexpr (MODE == ROUTED_K) {
+            if (k == 0) clear();   // whatever scales its stage of zeros met
+            k = next_k;
+        }
+        const int64_t n0 = at.n0 + wn * FN * 16;
+        int64_t m0 = at.m0 + wm * FM * 16;
+        // rows of this wave's part that are stored
+        const int row_first = at.first - (int)m0, row_last = at.last - (int)m0;
+        auto keeps = [&](int row) { return MODE != ROUTED_ROWS || (row >= row_first && row < row_last); };
+        if constexpr (MODE == ROUTED_K) m0 += (int64_t)at.group * A.M;
         int N = A.N;   // opaque here: else the offsets of every store are formed before the first tile and kept
         __asm__ volatile("" : "+s"(N));
         // Rows by way of LDS, 16 rows of 128 bytes at a time, so that 128 bytes of a row leave
@@ -541,7 +608,7 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void k_mx_matmul_tile(MatmulArgs A
                     for (int x = 0; x < 16; x += 8) {
                         const int row = x + (lane >> 3);
                         const v4u v = *reinterpret_cast<const v4u*>(mine + row * 128 + ((lane & 7) ^ ((row >> 1) & 7)) * 16);
-                        store<true>(reinterpret_cast<v4u*>(y + ((int64_t)(j * 16 + x) * N + h * 16) * kSize + off), v);
+                        if (keeps(j * 16 + row)) store<true>(reinterpret_cast<v4u*>(y + ((int64_t)(j * 16 + x) * N + h * 16) * kSize + off), v);
                     }
                     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
                 }
@@ -558,12 +625,23 @@ __global__ __launch_bounds__(64 * WN * WM, 2) void k_mx_matmul_tile(MatmulArgs A
                 for (int i = 0; i < FN; i++)
 #pragma unroll
                     for (int x = 0; x < 4; x++) {
+                        if (!keeps(j * 16 + r)) continue;
                         const uint32_t at = (uint32_t)(j * 16 + r) * N + i * 16 + g * 4 + x;
                         if (A.f32) store<false>(reinterpret_cast<float*>(y) + at, c[i][j][x]);
                         else store<false>(reinterpret_cast<uint16_t*>(y) + at, (uint16_t)bf16x2(c[i][j][x], 0.0f));
                     }
         }
     }
+}
+
+template <bool FP4B, bool FP4A, int TN, int TM, int WN, int WM>
+__global__ __launch_bounds__(64 * WN * WM, 2) void k_mx_matmul_tile(MatmulArgs A, int tiles_n, int tiles_m) {
+    mx_matmul_tiles<FP4B, FP4A, TN, TM, WN, WM, DENSE>(A, tiles_n, tiles_m, Routing{});
+}
+
+template <bool FP4B, bool FP4A, int TN, int TM, int WN, int WM, TileMode MODE>
+__global__ __launch_bounds__(64 * WN * WM, 2) void k_mx_matmul_routed_tile(MatmulArgs A, int tiles_n, int tiles_m, Routing routing) {
+    mx_matmul_tiles<FP4B, FP4A, TN, TM, WN, WM, MODE>(A, tiles_n, tiles_m, routing);
 }
 
 }  // namespace

@@ -1,0 +1,95 @@
+// Products of microscaled matrices grouped by a plan: few rows (or short
+// contractions) a group, from memory to registers.  The tiles of many rows are
+// lpq_mx_matmul.hpp's.
+//
+// Part of lpq_kernels.hip, which includes each part once, in this order: one
+// translation unit.
+#pragma once
+
+namespace {
+
+// ROUTED_ROWS: y[r] = a[r] b[group of r]^T, a workgroup takes up to 16 * MT rows of
+// one group and 16 * NT rows of its b.  ROUTED_K: y[g] = a[:, rows of g] b[:, rows
+// of g]^T, 16 * MT rows of a, 16 * NT of b.  As in k_mx_matmul_rows the waves share
+// out k in steps of 128 and add their results through LDS.
+template <bool FP4B, bool FP4A, int NT, int MT, int U, TileMode MODE>
+__global__ __launch_bounds__(64 * kRowsWaves) void k_mx_matmul_routed_rows(MatmulArgs A, int tiles_n, int tiles_m, Routing routing,
+                                                                           int first) {
+    constexpr int W = kRowsWaves;
+    __shared__ v4f part[W][NT * MT][64];
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, g = lane >> 4, r = lane & 15;
+    int tile = first + (int)blockIdx.x, group, k0 = 0, K = A.K;
+    int64_t m_first, m_last;
+    if constexpr (MODE == ROUTED_ROWS) {
+        RouteMap map;
+        map.open<16 * MT>(routing);
+        const int v = tile / tiles_n;
+        if (v >= map.total) return;   // the whole workgroup: the grid is for the most tiles there may be
+        const RouteTile t = map.find<16 * MT>(routing, v);
+        group = t.group;
+        m_first = t.first;
+        m_last = t.last;
+    } else {
+        group = tile / (tiles_n * tiles_m);
+        tile -= group * tiles_n * tiles_m;
+        const RouteRun run = route_run(routing, group);
+        k0 = run.first / 32 * 32;   // whole blocks: a plan with align 32 has no others
+        K = run.last / 32 * 32 - k0;
+        m_first = (int64_t)(tile / tiles_n) * 16 * MT;
+        m_last = A.M;
+    }
+    const int64_t n_first = (int64_t)(tile % tiles_n) * 16 * NT, b_first = MODE == ROUTED_ROWS ? (int64_t)group * A.N : 0;
+    const uint8_t *a[MT], *ae[MT], *b[NT], *be[NT];
+    bool in_m[MT], in_n[NT];
+    v4f c[NT][MT];
+#pragma unroll
+    for (int j = 0; j < NT; j++) {
+        const int64_t n = n_first + j * 16 + r;
+        in_n[j] = n < A.N;
+        const int64_t row = b_first + (in_n[j] ? n : 0);
+        b[j] = A.b + row * row_bytes<FP4B>(A.K) + row_bytes<FP4B>(k0);
+        be[j] = A.be + row * (A.K / 32) + k0 / 32;
+    }
+#pragma unroll
+    for (int i = 0; i < MT; i++) {
+        const int64_t m = m_first + i * 16 + r;
+        in_m[i] = m < m_last;
+        const int64_t row = in_m[i] ? m : m_first;
+        a[i] = A.a + row * row_bytes<FP4A>(A.K) + row_bytes<FP4A>(k0);
+        ae[i] = A.ae + row * (A.K / 32) + k0 / 32;
+#pragma unroll
+        for (int j = 0; j < NT; j++) c[j][i] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+    }
+    for (int k = wave * 128; k < K; k += W * 128 * U) {
+        Frag<FP4B> fb[U][NT];
+        Frag<FP4A> fa[U][MT];
+#pragma unroll
+        for (int u = 0; u < U; u++) {
+            const int at = k + u * W * 128;
+#pragma unroll
+            for (int j = 0; j < NT; j++) fb[u][j] = load_frag<FP4B>(b[j], be[j], in_n[j], at, K, g);
+#pragma unroll
+            for (int i = 0; i < MT; i++) fa[u][i] = load_frag<FP4A>(a[i], ae[i], in_m[i], at, K, g);
+        }
+#pragma unroll
+        for (int u = 0; u < U; u++)
+#pragma unroll
+            for (int j = 0; j < NT; j++)
+#pragma unroll
+                for (int i = 0; i < MT; i++) c[j][i] = mfma<FP4B, FP4A>(fb[u][j], fa[u][i], c[j][i]);
+    }
+#pragma unroll
+    for (int j = 0; j < NT; j++)
+#pragma unroll
+        for (int i = 0; i < MT; i++) part[wave][j * MT + i][lane] = c[j][i];
+    __syncthreads();
+    for (int x = wave; x < NT * MT; x += W) {
+        v4f s = part[0][x][lane];
+#pragma unroll
+        for (int w = 1; w < W; w++) s += part[w][x][lane];
+        const int64_t m = m_first + x % MT * 16 + r, n = n_first + x / MT * 16 + g * 4;
+        if (m < m_last && n < A.N) store_y4(A, MODE == ROUTED_ROWS ? m : (int64_t)group * A.M + m, (int)n, s);
+    }
+}
+
+}  // namespace

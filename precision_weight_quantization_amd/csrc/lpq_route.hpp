@@ -144,6 +144,68 @@ __global__ __launch_bounds__(kPlanThreads) void k_route_place(PlanArgs A) {
 }
 
 // ---------------------------------------------------------------------------
+// A plan as the products read it.  Offsets are cut to the buffer, so that whatever they
+// hold no row outside it is touched.
+struct Routing {
+    const int32_t* offsets;   // [groups + 1]
+    int32_t groups;
+    int32_t capacity;
+};
+struct RouteRun {
+    int first, last;   // rows [first, last) of a group
+};
+__device__ __forceinline__ RouteRun route_run(const Routing& R, int g) {
+    const int first = min(max(R.offsets[g], 0), R.capacity), last = min(R.offsets[g + 1], R.capacity);
+    return {first, max(first, last)};
+}
+
+// Tiles of TM rows of each group, end to end, without empty ones.  A lane counts the
+// tiles of its share of the groups once; a tile's group is then found by two ballots and
+// one round trip to memory, which is cheaper than a table in memory (another launch)
+// or in LDS (which the products' stages fill).
+struct RouteTile {
+    int group, first, last;
+};
+struct RouteMap {
+    int share, upto, mine, total;   // groups a lane; tiles up to and with its groups, of its groups; all
+    template <int TM>
+    static __device__ __forceinline__ int tiles(const RouteRun& r) {
+        return (r.last - r.first + TM - 1) / TM;
+    }
+    static __device__ __forceinline__ int scan(int v, int lane, int width) {
+        for (int d = 1; d < width; d *= 2) {
+            const int up = __shfl_up(v, d);
+            if (lane >= d) v += up;
+        }
+        return v;
+    }
+    template <int TM>
+    __device__ __forceinline__ void open(const Routing& R) {
+        const int lane = threadIdx.x & 63;
+        share = (R.groups + 63) / 64;
+        mine = 0;
+        for (int i = 0; i < share; i++)
+            if (lane * share + i < R.groups) mine += tiles<TM>(route_run(R, lane * share + i));
+        upto = scan(mine, lane, 64);
+        total = min(__builtin_amdgcn_readlane(upto, 63), R.capacity / TM + R.groups);   // ordered offsets have no more
+    }
+    // Tile v < total, the same in every lane.
+    template <int TM>
+    __device__ __forceinline__ RouteTile find(const Routing& R, int v) const {
+        const int lane = threadIdx.x & 63;
+        const int l = __builtin_ctzll(__builtin_amdgcn_ballot_w64(upto > v));
+        v -= __builtin_amdgcn_readlane(upto - mine, l);
+        const int g = l * share + lane;
+        RouteRun run{};
+        if (lane < share && g < R.groups) run = route_run(R, g);
+        const int own = tiles<TM>(run), sum = scan(own, lane, share);
+        const int i = __builtin_ctzll(__builtin_amdgcn_ballot_w64(sum > v));
+        const int begin = __builtin_amdgcn_readlane(run.first, i) + (v - __builtin_amdgcn_readlane(sum - own, i)) * TM;
+        return {l * share + i, begin, min(begin + TM, __builtin_amdgcn_readlane(run.last, i))};
+    }
+};
+
+// ---------------------------------------------------------------------------
 // Work on whole rows in vectors of 8 elements, one to a thread: the workgroups
 // behind the first `pad_groups` (see zero_rows) hold the tokens' vectors end to end.
 constexpr int kRouteThreads = 256;

@@ -82,9 +82,126 @@ lpq_status route_gather(const uint16_t* x, int64_t tokens, int64_t N, const int3
     return launched();
 }
 
+// The checks of a routed product: a [M, K], b [rows_b, K], y of ny elements, and the plan's offsets.
+struct RoutedProduct {
+    const uint8_t *a, *ae, *b, *be;
+    int a_format, b_format;
+    const int32_t* offsets;
+    int32_t groups;
+    int64_t M, rows_b, N, K, ny;
+    void* y;
+    int y_type;
+};
+lpq_status check_routed(const RoutedProduct& P) {
+    if (!P.a || !P.ae || !P.b || !P.be || !P.y || !P.offsets) return LPQ_ERR_NULL;
+    const bool a4 = P.a_format == LPQ_MXFP4, b4 = P.b_format == LPQ_MXFP4;
+    if ((!a4 && P.a_format != LPQ_MXFP8) || (!b4 && P.b_format != LPQ_MXFP8)) return LPQ_ERR_ARG;
+    if (P.y_type != LPQ_BF16 && !(P.y_type == LPQ_F32 && a4 && b4)) return LPQ_ERR_ARG;
+    if (!aligned(P.a, 16) || !aligned(P.b, 16) || !aligned(P.y, 16) || !aligned(P.offsets, 4)) return LPQ_ERR_ALIGN;
+    if (any_overlap({range(P.y, P.ny * (P.y_type == LPQ_F32 ? 4 : 2))},
+                    {range(P.a, P.M * P.K / (a4 ? 2 : 1)), range(P.ae, P.M * P.K / 32), range(P.b, P.rows_b * P.K / (b4 ? 2 : 1)),
+                     range(P.be, P.rows_b * P.K / 32), range(P.offsets, 4 * (P.groups + 1))}))
+        return LPQ_ERR_ARG;
+    return LPQ_OK;
+}
+
+template <bool FP4A, bool FP4B, TileMode MODE>
+struct RoutedLaunch {
+    MatmulArgs A;
+    Routing R;
+    hipStream_t s;
+
+    // Row tiles of 16 * MT rows, in all groups together, at most.
+    int64_t row_tiles(int64_t tm) const {
+        const int64_t most = R.capacity < R.groups ? R.capacity : R.groups;
+        return R.capacity / tm + most;
+    }
+    template <int NT, int MT, int U>
+    lpq_status rows() const {
+        const int64_t tiles_n = ceil_div(A.N, 16 * NT), tiles_m = MODE == ROUTED_K ? ceil_div(A.M, 16 * MT) : 1;
+        const int64_t tiles = MODE == ROUTED_K ? tiles_n * tiles_m * R.groups : tiles_n * row_tiles(16 * MT);
+        const int64_t most = max_groups(64 * kRowsWaves);
+        if (tiles > 0x7fffffffLL) return LPQ_ERR_SHAPE;   // tile indexes are 32-bit
+        for (int64_t first = 0; first < tiles; first += most) {
+            hipLaunchKernelGGL((k_mx_matmul_routed_rows<FP4B, FP4A, NT, MT, U, MODE>),
+                               dim3((unsigned)(tiles - first < most ? tiles - first : most)), dim3(64 * kRowsWaves), 0, s, A,
+                               (int)tiles_n, (int)tiles_m, R, (int)first);
+            const lpq_status st = launched();
+            if (st != LPQ_OK) return st;
+        }
+        return LPQ_OK;
+    }
+    template <int TN, int TM, int WN, int WM>
+    lpq_status tile() const {
+        const int64_t nt = ceil_div(A.N, TN), mt = MODE == ROUTED_K ? ceil_div(A.M, TM) : row_tiles(TM);
+        const int64_t tiles = MODE == ROUTED_K ? nt * mt * R.groups : nt * mt;
+        if (tiles > 0x7fffffffLL) return LPQ_ERR_SHAPE;
+        const int64_t most = kComputeUnits * (TN == 256 ? 1 : 2);
+        hipLaunchKernelGGL((k_mx_matmul_routed_tile<FP4B, FP4A, TN, TM, WN, WM, MODE>), dim3((unsigned)(tiles < most ? tiles : most)),
+                           dim3(64 * WN * WM), 0, s, A, (int)nt, (int)mt, R);
+        return launched();
+    }
+};
+
+template <bool FP4A, bool FP4B>
+lpq_status mx_matmul_routed(const MatmulArgs& A, const Routing& R, hipStream_t s) {
+    const RoutedLaunch<FP4A, FP4B, ROUTED_ROWS> L{A, R, s};
+    const int64_t average = R.capacity / R.groups;
+    const bool limits = A.K > 128 * stage_steps<FP4B, FP4A>() && A.K <= (1 << 22) && A.N <= (1 << 22);
+    if (limits && average >= 64 && A.N >= 128 && R.capacity >= 128) {
+        if (average >= 192 && A.N >= 256 && R.capacity >= 256) return L.template tile<256, 256, 2, 4>();
+        return L.template tile<128, 128, 2, 2>();
+    }
+    if (average <= 16) return L.template rows<1, 1, 1>();
+    return average <= 32 ? L.template rows<2, 2, 1>() : L.template rows<2, 4, 1>();
+}
+
+template <bool FP4A, bool FP4B>
+lpq_status mx_matmul_routed_dw(const MatmulArgs& A, const Routing& R, hipStream_t s) {
+    const RoutedLaunch<FP4A, FP4B, ROUTED_K> L{A, R, s};
+    const bool limits = A.K <= (1 << 22) && A.N <= (1 << 22);
+    if (limits && A.M >= 128 && A.N >= 128) {
+        if (A.M >= 256 && A.N >= 256) return L.template tile<256, 256, 2, 4>();
+        return L.template tile<128, 128, 2, 2>();
+    }
+    return L.template rows<2, 2, 1>();
+}
+
 }  // namespace
 
 extern "C" {
+
+lpq_status lpq_mx_matmul_routed(const uint8_t* a, const uint8_t* ae, int a_format, const uint8_t* b, const uint8_t* be, int b_format,
+                                const int32_t* offsets, int32_t groups, int64_t capacity, int64_t N, int64_t K, void* y, int y_type,
+                                void* stream) {
+    const int64_t most = int64_t(1) << 40;
+    if (groups <= 0 || groups > kRouteMaxGroups || capacity <= 0 || N <= 0 || K <= 0 || K % 32) return LPQ_ERR_SHAPE;
+    if (capacity > kRouteMaxRows || N > kRouteMaxRows || K > kRouteMaxRows) return LPQ_ERR_SHAPE;
+    if (capacity > most / N || capacity > most / K || N > most / K / groups) return LPQ_ERR_SHAPE;
+    const lpq_status st = check_routed({a, ae, b, be, a_format, b_format, offsets, groups, capacity, groups * N, N, K, capacity * N, y, y_type});
+    if (st != LPQ_OK) return st;
+    const MatmulArgs A{a, ae, b, be, y, (int32_t)capacity, (int32_t)N, (int32_t)K, y_type == LPQ_F32};
+    const Routing R{offsets, groups, (int32_t)capacity};
+    const hipStream_t s = (hipStream_t)stream;
+    if (a_format == LPQ_MXFP4) return b_format == LPQ_MXFP4 ? mx_matmul_routed<true, true>(A, R, s) : mx_matmul_routed<true, false>(A, R, s);
+    return b_format == LPQ_MXFP4 ? mx_matmul_routed<false, true>(A, R, s) : mx_matmul_routed<false, false>(A, R, s);
+}
+
+lpq_status lpq_mx_matmul_routed_dw(const uint8_t* a, const uint8_t* ae, int a_format, const uint8_t* b, const uint8_t* be,
+                                   int b_format, const int32_t* offsets, int32_t groups, int64_t M, int64_t N, int64_t capacity,
+                                   void* y, int y_type, void* stream) {
+    const int64_t most = int64_t(1) << 40;
+    if (groups <= 0 || groups > kRouteMaxGroups || M <= 0 || N <= 0 || capacity <= 0 || capacity % 32) return LPQ_ERR_SHAPE;
+    if (capacity > kRouteMaxRows || M > kRouteMaxRows || N > kRouteMaxRows) return LPQ_ERR_SHAPE;
+    if (M > most / capacity || N > most / capacity || M > most / N / groups) return LPQ_ERR_SHAPE;
+    const lpq_status st = check_routed({a, ae, b, be, a_format, b_format, offsets, groups, M, N, N, capacity, groups * M * N, y, y_type});
+    if (st != LPQ_OK) return st;
+    const MatmulArgs A{a, ae, b, be, y, (int32_t)M, (int32_t)N, (int32_t)capacity, y_type == LPQ_F32};
+    const Routing R{offsets, groups, (int32_t)capacity};
+    const hipStream_t s = (hipStream_t)stream;
+    if (a_format == LPQ_MXFP4) return b_format == LPQ_MXFP4 ? mx_matmul_routed_dw<true, true>(A, R, s) : mx_matmul_routed_dw<true, false>(A, R, s);
+    return b_format == LPQ_MXFP4 ? mx_matmul_routed_dw<false, true>(A, R, s) : mx_matmul_routed_dw<false, false>(A, R, s);
+}
 
 int64_t lpq_route_capacity(int64_t pairs, int32_t groups, int32_t align) { return route_capacity(pairs, groups, align); }
 

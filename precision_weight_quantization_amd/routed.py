@@ -108,6 +108,58 @@ def lpq_route_gather_mxfp4(x, rows, src, p=None, e=None, stream=None):
     return p, e
 
 
+# --------------------------------------------------------------------------- products
+
+def _offsets(offsets, like):
+    groups = _arg(offsets, "offsets", like, dtypes=_I32, dims=1).numel() - 1
+    if groups < 1:
+        raise ValueError("offsets holds groups + 1 numbers")
+    return groups
+
+
+def _out_type(out_dtype):
+    if out_dtype not in _p._MX_OUT:
+        raise TypeError(f"out_dtype must be one of {[str(d) for d in _p._MX_OUT]}, got {out_dtype}")
+    return _p._MX_OUT[out_dtype], 4 if out_dtype == torch.float32 else 2
+
+
+def lpq_mx_matmul_routed(a, ae, b, be, offsets, out_dtype=torch.bfloat16, y=None, a_format=None, b_format=None, stream=None):
+    """y [R,N], y[r] = a[r] b[group of r]^T: a [R,K] codes in a plan's order with scale bytes ae, b [groups,N,K] the
+    groups' weights with be [groups,N,K/32], offsets [groups+1] the plan's.  Rows of no group are left as they were
+    (not set in a y that is allocated here).  Formats and types as in lpq_mx_matmul."""
+    fa, R, K = _p._mx_operand(a, ae, a_format, "a")
+    groups = _offsets(offsets, a)
+    _arg(b, "b", a, esize=1, dims=3)
+    if b.shape[0] != groups:
+        raise ValueError(f"b holds {b.shape[0]} groups' weights, offsets are of {groups}")
+    fb, rows, Kb = _p._mx_operand(b.view(-1, b.shape[2]), be, b_format, "b", a)
+    if K != Kb:
+        raise ValueError(f"a has {K} columns, b {Kb}")
+    N = rows // groups
+    kind, size = _out_type(out_dtype)
+    with _on(stream, a):
+        y, = _outs(a, (y, "y", size * R * N, (R, N), out_dtype, size))
+    _launch(_p._L.lpq_mx_matmul_routed, "lpq_mx_matmul_routed", a, stream, a.data_ptr(), ae.data_ptr(), fa, b.data_ptr(),
+            be.data_ptr(), fb, offsets.data_ptr(), groups, R, N, K, y.data_ptr(), kind)
+    return y
+
+
+def lpq_mx_matmul_routed_dw(a, ae, b, be, offsets, out_dtype=torch.bfloat16, y=None, a_format=None, b_format=None, stream=None):
+    """y [groups,M,N], y[g] = a[:, rows of g] b[:, rows of g]^T: a [M,R] and b [N,R] the transposed forms of gathered
+    rows (a plan with align 32), offsets [groups+1] the plan's.  Zeros for a group without rows."""
+    fa, M, R = _p._mx_operand(a, ae, a_format, "a")
+    fb, N, Rb = _p._mx_operand(b, be, b_format, "b", a)
+    if R != Rb:
+        raise ValueError(f"a has {R} columns, b {Rb}")
+    groups = _offsets(offsets, a)
+    kind, size = _out_type(out_dtype)
+    with _on(stream, a):
+        y, = _outs(a, (y, "y", size * groups * M * N, (groups, M, N), out_dtype, size))
+    _launch(_p._L.lpq_mx_matmul_routed_dw, "lpq_mx_matmul_routed_dw", a, stream, a.data_ptr(), ae.data_ptr(), fa, b.data_ptr(),
+            be.data_ptr(), fb, offsets.data_ptr(), groups, M, N, R, y.data_ptr(), kind)
+    return y
+
+
 # --------------------------------------------------------------------------- combination
 
 def lpq_route_combine(y, rows, weights=None, residual=None, out=None, stream=None):

@@ -83,6 +83,23 @@ def test_combine_refusals(lib):
     assert L.lpq_last_hip_error() == 0
 
 
+def test_product_refusals(lib):
+    L = lib.raw()
+    call = caller(L.lpq_mx_matmul_routed, a=Q[0], ae=Q[1], fa=0, b=Q[2], be=Q[3], fb=1, off=Q[4], groups=3, R=64, N=128, K=256, y=Q[5],
+                  type=0, stream=None)
+    dw = caller(L.lpq_mx_matmul_routed_dw, a=Q[0], ae=Q[1], fa=0, b=Q[2], be=Q[3], fb=1, off=Q[4], groups=3, M=64, N=128, R=256, y=Q[5],
+                type=0, stream=None)
+    for f in (call, dw):
+        refusals(f, 1, *({k: None} for k in ("a", "ae", "b", "be", "off", "y")))
+        refusals(f, 2, dict(groups=0), dict(groups=1025), dict(R=0), dict(N=0), dict(R=(1 << 30) + 32), dict(N=(1 << 30) + 1),
+                 dict(R=1 << 28, N=1 << 13))
+        refusals(f, 3, dict(a=Q[0] + 8), dict(b=Q[2] + 8), dict(y=Q[5] + 8), dict(off=Q[4] + 2))
+        refusals(f, 6, dict(fa=2), dict(fb=-1), dict(type=2), dict(type=1), dict(type=1, fa=1, fb=0), dict(y=Q[0]), dict(y=Q[3]), dict(y=Q[4]))
+    refusals(call, 2, dict(K=0), dict(K=48), dict(K=(1 << 30) + 32), dict(N=1 << 15, K=1 << 24), dict(R=1 << 28, K=1 << 13))
+    refusals(dw, 2, dict(M=0), dict(M=(1 << 30) + 1), dict(R=48), dict(M=1 << 20, N=1 << 19), dict(M=1 << 28, R=1 << 13))
+    assert L.lpq_last_hip_error() == 0
+
+
 def bf(*s):
     return fake(torch.zeros(s, dtype=torch.bfloat16))
 
@@ -133,6 +150,24 @@ def test_route_binding(lib, recorder):
     assert recorder.calls == []
 
 
+def test_product_binding(lib, recorder):
+    f8 = lambda *s: fake(torch.zeros(s, dtype=torch.uint8).view(torch.float8_e4m3fn))
+    a, ae, b, be, off = f8(8, 64), u8(8, 2), u8(3, 16, 32), u8(3, 16, 2), i32(4)
+    f = lib.lpq_mx_matmul_routed
+    refused([(TypeError, lambda: f(bf(8, 64), ae, b, be, off)), (ValueError, lambda: f(a, u8(8, 1), b, be, off)),
+             (ValueError, lambda: f(a, ae, u8(16, 32), be, off)), (ValueError, lambda: f(a, ae, b, u8(3, 16, 1), off)),
+             (ValueError, lambda: f(a, ae, u8(3, 16, 16), u8(3, 16, 1), off)), (ValueError, lambda: f(a, ae, b, be, i32(3))),
+             (TypeError, lambda: f(a, ae, b, be, fake(torch.zeros(4, dtype=torch.int64)))), (ValueError, lambda: f(a, ae, b, be, i32(1))),
+             (TypeError, lambda: f(a, ae, b, be, off, out_dtype=torch.float16)), (ValueError, lambda: f(a, ae, b, be, off, y=bf(8, 15))),
+             (TypeError, lambda: f(a, ae, b, be, off, y=f32(8, 16))), (ValueError, lambda: f(a, ae, b, be, off, b_format="int4"))])
+    a, ae, b, be = f8(16, 64), u8(16, 2), f8(24, 64), u8(24, 2)
+    f = lib.lpq_mx_matmul_routed_dw
+    refused([(ValueError, lambda: f(a, ae, f8(24, 32), u8(24, 1), off)), (ValueError, lambda: f(a, ae, b, u8(23, 2), off)),
+             (ValueError, lambda: f(a, ae, b, be, i32(2, 2))), (ValueError, lambda: f(a, ae, b, be, off, y=bf(3, 16, 23))),
+             (TypeError, lambda: f(a, ae, b, be, f32(4)))])
+    assert recorder.calls == []
+
+
 # ----------------------------------------------------------------------------- device and stream
 
 def on1(dtype, *shape):
@@ -147,6 +182,9 @@ CALLS = {
     "lpq_route_gather": lambda **k: lpq.lpq_route_gather(x(), rows(), src(), y(), **k),
     "lpq_route_gather_mxfp8": lambda **k: lpq.lpq_route_gather_mxfp8(x(), rows(), src(), q(), e(), **k),
     "lpq_route_gather_mxfp4": lambda **k: lpq.lpq_route_gather_mxfp4(x(), rows(), src(), p(), e(), **k),
+    "lpq_mx_matmul_routed": lambda **k: lpq.lpq_mx_matmul_routed(p(), e(), on1(U8, 4, 16, 32), on1(U8, 4, 16, 2), on1(I32, 5),
+                                                                 y=on1(BF, 8, 16), **k),
+    "lpq_mx_matmul_routed_dw": lambda **k: lpq.lpq_mx_matmul_routed_dw(p(), e(), p(), e(), on1(I32, 5), y=on1(BF, 4, 8, 8), **k),
     "lpq_route_combine": lambda **k: lpq.lpq_route_combine(y(), rows(), weights(), x(), x(), **k),
     "lpq_route_combine_backward": lambda **k: lpq.lpq_route_combine_backward(x(), rows(), src(), weights(), y(), y(), weights(), **k),
 }
