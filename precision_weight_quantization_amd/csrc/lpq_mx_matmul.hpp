@@ -233,6 +233,16 @@ __device__ __forceinline__ void static_for(F&& f) {
 // b (ragged m); or products over runs of the contraction, each with its own y (ragged k).
 enum TileMode { DENSE, ROUTED_ROWS, ROUTED_K };
 
+// The tiles of TM rows of each group; nothing in the other modes.
+template <TileMode MODE, int TM>
+struct RowMap {
+    __device__ __forceinline__ RowMap(const Routing&) {}
+};
+template <int TM>
+struct RowMap<ROUTED_ROWS, TM> : RouteMap<RowTiles<TM>> {
+    __device__ __forceinline__ RowMap(const Routing& R) : RouteMap<RowTiles<TM>>(R, RowTiles<TM>{}) {}
+};
+
 // N >= TN, M >= TM; DENSE and ROUTED_ROWS: at least two stages.  ROUTED_ROWS: b [groups, N, K], y's
 // rows of no group stay as they are.  ROUTED_K: operands [., K] of all groups, y [groups, M, N].
 template <bool FP4B, bool FP4A, int TN, int TM, int WN, int WM, TileMode MODE>
@@ -265,14 +275,27 @@ __device__ __forceinline__ void mx_matmul_tiles(const MatmulArgs& A, int tiles_n
     auto steps_of = [&](int k) { return MODE == ROUTED_K ? max((k + BK - 1) / BK, 1) : dense_steps; };
 
     // this workgroup's tiles: every slots-th of its XCD's run
-    RouteMap map;
-    if constexpr (MODE == ROUTED_ROWS) {
-        map.open<TM>(routing);
-        tiles_m = map.total;
+    const RowMap<MODE, TM> map(routing);
+    if constexpr (MODE == ROUTED_ROWS) tiles_m = min(map.total, routing.capacity / TM + routing.groups);   // no plan has more
+    const int total = tiles_n * tiles_m, xcd = blockIdx.x % kXcds, each = total / kXcds, more = total % kXcds;
+    int run = xcd * each + min(xcd, more), run_end = run + each + (xcd < more);
+    if constexpr (MODE == ROUTED_K) {
+        // The tiles of a group take as long as its contraction, so an XCD's run is its share of that
+        // rather than of the tiles (65536 rows of uneven groups, 1536 x 2048: 530 us by tiles).  In
+        // stages, where a tile's stores and start count as one, and as three at least.
+        const RouteMap cost(routing, [&](const RouteRun& r) { return max(steps_of(r.last / 32 * 32 - r.first / 32 * 32), 3) + 1; });
+        const int xcds = min(kXcds, (int)gridDim.x);
+        auto border = [&](int x) {   // the first tile of XCD x
+            const int at = (int)((int64_t)cost.total * x / xcds);
+            if (at >= cost.total) return total * routing.groups;
+            RouteRun r;
+            int within;
+            const int g = cost.find(routing, at, r, within);
+            return min(g * total + (int)((int64_t)within * total / cost.count(r)), total * routing.groups);
+        };
+        run = border(xcd);
+        run_end = border(xcd + 1);
     }
-    const int each_group = tiles_n * tiles_m;
-    const int total = MODE == ROUTED_K ? each_group * routing.groups : each_group, xcd = blockIdx.x % kXcds, each = total / kXcds, more = total % kXcds;
-    const int run = xcd * each + min(xcd, more), run_end = run + each + (xcd < more);
     const int slots = ((int)gridDim.x - xcd + kXcds - 1) / kXcds;
 
     // a lane's offsets from the first row of a load (below 2^31: K is limited by the caller)
@@ -283,6 +306,7 @@ __device__ __forceinline__ void mx_matmul_tiles(const MatmulArgs& A, int tiles_n
 
     // The last tile of a row or column ends with the matrix: it repeats some of its neighbour's
     // results.
+    const bool whole_lines = MODE == DENSE || (int64_t)A.N * (A.f32 ? 4 : 2) % 128 == 0;
     // A routed tile of rows that passes the buffer's end begins earlier; it stores its group's rows only.
     struct Tile {
         int64_t n0, m0;
@@ -294,20 +318,21 @@ __device__ __forceinline__ void mx_matmul_tiles(const MatmulArgs& A, int tiles_n
         Tile t{};
         int n, m;
         if constexpr (MODE == ROUTED_K) {
-            t.group = tile / each_group;
-            tile -= t.group * each_group;
-            const RouteRun run = route_run(routing, t.group);
+            t.group = tile / total;
+            tile -= t.group * total;
+            const RouteRun run = wave_run(routing, t.group);
             t.k = run.last / 32 * 32 - run.first / 32 * 32;   // whole blocks: a plan with align 32 has no others
             t.k0 = min(run.first / 32 * 32, A.K - 32);
         }
         tile_at(tile, tiles_n, tiles_m, n, m);
         t.n0 = min((int64_t)n * TN, (int64_t)A.N - TN);
         if constexpr (MODE == ROUTED_ROWS) {
-            const RouteTile r = map.find<TM>(routing, m);
-            t.group = r.group;
-            t.first = r.first;
-            t.last = r.last;
-            t.m0 = min(r.first, A.M - TM);
+            RouteRun r;
+            int within;
+            t.group = map.find(routing, m, r, within);
+            t.first = r.first + within * TM;
+            t.last = min(t.first + TM, r.last);
+            t.m0 = min(t.first, A.M - TM);
         } else {
             t.m0 = min((int64_t)m * TM, (int64_t)A.M - TM);
         }
@@ -502,6 +527,7 @@ __device__ __forceinline__ void mx_matmul_tiles(const MatmulArgs& A, int tiles_n
     open_tile();
     int k = A.K, next_k = A.K;   // of the tile that is computed, and of the next one
     if constexpr (MODE == ROUTED_K) k = load_k;
+    Tile tile_now = tile_of(first_tile), tile_next = tile_now;
     load_stage(0);
     put_scales(0);
     lds_arrived();
@@ -523,9 +549,15 @@ __device__ __forceinline__ void mx_matmul_tiles(const MatmulArgs& A, int tiles_n
     for (int tile = first_tile; tile < run_end; tile += slots) {
         clear();
         const int steps = steps_of(k);
-        if constexpr (MODE == ROUTED_K)
-            if (tile + slots < run_end) next_k = tile_of(tile + slots).k;
+        if constexpr (MODE != DENSE)
+            if (tile + slots < run_end) tile_next = tile_of(tile + slots);
+        if constexpr (MODE == ROUTED_K) next_k = tile_next.k;
+        // A wave whose rows are all behind its group's last has no products to do: it helps with the loads only,
+        // and leaves the matrix cores to the others.
+        const int wave_row = tile_now.m0 + wm * FM * 16;
+        const bool busy = MODE != ROUTED_ROWS || (wave_row < tile_now.last && wave_row + FM * 16 > tile_now.first);
         for (int s = 0; s < steps; s++) {
+            if (busy)
             static_for<FN * KS - 1>([&](auto at) {
                 constexpr int x = decltype(at)::value, i = x % FN, ks = x / FN;
                 Frag<FP4B> next = fb[kAhead - 1];
@@ -561,13 +593,19 @@ __device__ __forceinline__ void mx_matmul_tiles(const MatmulArgs& A, int tiles_n
 #pragma unroll
             for (int i = 0; i < kAhead; i++) next[i] = frag_b(i, 0);
             const Scales next_sv = read_scales(0);
-            products(std::integral_constant<int, FN - 1>{}, [&](int j) { fa[j] = frag_a(j, 0); });
+            if (busy) {
+                products(std::integral_constant<int, FN - 1>{}, [&](int j) { fa[j] = frag_a(j, 0); });
+            } else {
+#pragma unroll
+                for (int j = 0; j < FM; j++) fa[j] = frag_a(j, 0);
+            }
             sv = next_sv;
 #pragma unroll
             for (int i = 0; i < kAhead; i++) fb[i] = next[i];
             pin();
         }
-        const Tile at = tile_of(tile);
+        const Tile at = MODE == DENSE ? tile_of(tile) : tile_now;
+        tile_now = tile_next;
         if constexpr (MODE == ROUTED_K) {
             if (k == 0) clear();   // whatever scales its stage of zeros met
             k = next_k;
@@ -583,8 +621,9 @@ __device__ __forceinline__ void mx_matmul_tiles(const MatmulArgs& A, int tiles_n
         // Rows by way of LDS, 16 rows of 128 bytes at a time, so that 128 bytes of a row leave
         // in one piece: stored from the accumulators each instruction would write 32 bytes of
         // 16 rows (measured: 17 us of 233 at 8192 x 9728 x 2560).  Swizzled as a stage's rows
-        // are.  Non-temporal: 9 us of 207 there.
-        auto store_rows = [&](auto f32) {
+        // are.  Non-temporal: 9 us of 207 there; but not in parts of lines, which then are
+        // joined in memory (96 results of 520 x 776 in FP32: 133 us and 54).
+        auto store_rows = [&](auto f32, auto nt) {
             constexpr bool F32 = decltype(f32)::value;
             constexpr int kSize = F32 ? 4 : 2, kFrags = F32 ? 2 : 4;   // 16-column results in 128 bytes
             uint8_t* mine = lds + kOut + wave * 2048;
@@ -608,15 +647,22 @@ __device__ __forceinline__ void mx_matmul_tiles(const MatmulArgs& A, int tiles_n
                     for (int x = 0; x < 16; x += 8) {
                         const int row = x + (lane >> 3);
                         const v4u v = *reinterpret_cast<const v4u*>(mine + row * 128 + ((lane & 7) ^ ((row >> 1) & 7)) * 16);
-                        if (keeps(j * 16 + row)) store<true>(reinterpret_cast<v4u*>(y + ((int64_t)(j * 16 + x) * N + h * 16) * kSize + off), v);
+                        v4u* to = reinterpret_cast<v4u*>(y + ((int64_t)(j * 16 + x) * N + h * 16) * kSize + off);
+                        if (!keeps(j * 16 + row)) continue;
+                        store<decltype(nt)::value>(to, v);
                     }
                     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
                 }
             }
         };
         if (A.f32 ? N % 4 == 0 : N % 8 == 0) {
-            if (A.f32) store_rows(std::true_type{});
-            else store_rows(std::false_type{});
+            if (whole_lines) {
+                if (A.f32) store_rows(std::true_type{}, std::true_type{});
+                else store_rows(std::false_type{}, std::true_type{});
+            } else {
+                if (A.f32) store_rows(std::true_type{}, std::false_type{});
+                else store_rows(std::false_type{}, std::false_type{});
+            }
         } else {
             uint8_t* y = static_cast<uint8_t*>(A.y) + (m0 * N + n0) * (A.f32 ? 4 : 2);
 #pragma unroll

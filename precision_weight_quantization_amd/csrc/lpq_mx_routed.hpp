@@ -21,18 +21,18 @@ __global__ __launch_bounds__(64 * kRowsWaves) void k_mx_matmul_routed_rows(Matmu
     int tile = first + (int)blockIdx.x, group, k0 = 0, K = A.K;
     int64_t m_first, m_last;
     if constexpr (MODE == ROUTED_ROWS) {
-        RouteMap map;
-        map.open<16 * MT>(routing);
+        const RouteMap map(routing, RowTiles<16 * MT>{});
         const int v = tile / tiles_n;
         if (v >= map.total) return;   // the whole workgroup: the grid is for the most tiles there may be
-        const RouteTile t = map.find<16 * MT>(routing, v);
-        group = t.group;
-        m_first = t.first;
-        m_last = t.last;
+        RouteRun r;
+        int within;
+        group = map.find(routing, v, r, within);
+        m_first = r.first + within * 16 * MT;
+        m_last = min(r.first + (within + 1) * 16 * MT, r.last);
     } else {
         group = tile / (tiles_n * tiles_m);
         tile -= group * tiles_n * tiles_m;
-        const RouteRun run = route_run(routing, group);
+        const RouteRun run = wave_run(routing, group);
         k0 = run.first / 32 * 32;   // whole blocks: a plan with align 32 has no others
         K = run.last / 32 * 32 - k0;
         m_first = (int64_t)(tile / tiles_n) * 16 * MT;

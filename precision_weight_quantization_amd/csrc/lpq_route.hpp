@@ -154,55 +154,66 @@ struct Routing {
 struct RouteRun {
     int first, last;   // rows [first, last) of a group
 };
-__device__ __forceinline__ RouteRun route_run(const Routing& R, int g) {
-    const int first = min(max(R.offsets[g], 0), R.capacity), last = min(R.offsets[g + 1], R.capacity);
+__device__ __forceinline__ RouteRun route_run(const Routing& R, int from, int to) {
+    const int first = min(max(from, 0), R.capacity), last = min(to, R.capacity);
     return {first, max(first, last)};
 }
+// Of a group of the lane's own.
+__device__ __forceinline__ RouteRun lane_run(const Routing& R, int g) {
+    return route_run(R, load<false>(R.offsets + g), load<false>(R.offsets + g + 1));
+}
+// Of one group for the whole wave.  Read through the scalar cache: a vector load would wait for
+// all earlier ones of the wave, a product's next stages among them.
+__device__ __forceinline__ int wave_offset(const Routing& R, int g) {
+    return ((__attribute__((address_space(4))) const int32_t*)R.offsets)[__builtin_amdgcn_readfirstlane(g)];
+}
+__device__ __forceinline__ RouteRun wave_run(const Routing& R, int g) { return route_run(R, wave_offset(R, g), wave_offset(R, g + 1)); }
 
-// Tiles of TM rows of each group, end to end, without empty ones.  A lane counts the
-// tiles of its share of the groups once; a tile's group is then found by two ballots and
-// one round trip to memory, which is cheaper than a table in memory (another launch)
-// or in LDS (which the products' stages fill).
-struct RouteTile {
-    int group, first, last;
-};
+__device__ __forceinline__ int wave_scan(int v) {   // inclusive sums over the lanes
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+        const int up = __shfl_up(v, d);
+        if (lane >= d) v += up;
+    }
+    return v;
+}
+
+// Something that each group has a number of, end to end: tiles of its rows, or the cost of
+// its contraction.  A lane counts for its share of the groups once; the group of a place is
+// then found by a ballot and scalar loads of that lane's share, which is cheaper than a table
+// in memory (another launch) or in LDS (which the products' stages fill).
+template <typename Count>
 struct RouteMap {
-    int share, upto, mine, total;   // groups a lane; tiles up to and with its groups, of its groups; all
-    template <int TM>
-    static __device__ __forceinline__ int tiles(const RouteRun& r) {
-        return (r.last - r.first + TM - 1) / TM;
-    }
-    static __device__ __forceinline__ int scan(int v, int lane, int width) {
-        for (int d = 1; d < width; d *= 2) {
-            const int up = __shfl_up(v, d);
-            if (lane >= d) v += up;
-        }
-        return v;
-    }
-    template <int TM>
-    __device__ __forceinline__ void open(const Routing& R) {
+    Count count;                    // of a run of rows
+    int share, upto, mine, total;   // groups a lane; counts up to and with its groups, of its groups; of all
+    __device__ __forceinline__ RouteMap(const Routing& R, Count c) : count(c) {
         const int lane = threadIdx.x & 63;
         share = (R.groups + 63) / 64;
         mine = 0;
         for (int i = 0; i < share; i++)
-            if (lane * share + i < R.groups) mine += tiles<TM>(route_run(R, lane * share + i));
-        upto = scan(mine, lane, 64);
-        total = min(__builtin_amdgcn_readlane(upto, 63), R.capacity / TM + R.groups);   // ordered offsets have no more
+            if (lane * share + i < R.groups) mine += count(lane_run(R, lane * share + i));
+        upto = wave_scan(mine);
+        total = __builtin_amdgcn_readlane(upto, 63);
     }
-    // Tile v < total, the same in every lane.
-    template <int TM>
-    __device__ __forceinline__ RouteTile find(const Routing& R, int v) const {
-        const int lane = threadIdx.x & 63;
+    // The group of place v < total, the same in every lane; its run, and the place within it.
+    __device__ __forceinline__ int find(const Routing& R, int v, RouteRun& run, int& within) const {
         const int l = __builtin_ctzll(__builtin_amdgcn_ballot_w64(upto > v));
-        v -= __builtin_amdgcn_readlane(upto - mine, l);
-        const int g = l * share + lane;
-        RouteRun run{};
-        if (lane < share && g < R.groups) run = route_run(R, g);
-        const int own = tiles<TM>(run), sum = scan(own, lane, share);
-        const int i = __builtin_ctzll(__builtin_amdgcn_ballot_w64(sum > v));
-        const int begin = __builtin_amdgcn_readlane(run.first, i) + (v - __builtin_amdgcn_readlane(sum - own, i)) * TM;
-        return {l * share + i, begin, min(begin + TM, __builtin_amdgcn_readlane(run.last, i))};
+        within = v - __builtin_amdgcn_readlane(upto - mine, l);
+        int g = l * share, from = wave_offset(R, g);
+        for (;; g++) {
+            const int to = wave_offset(R, g + 1);
+            run = route_run(R, from, to);
+            const int n = count(run);
+            if (within < n || g + 1 >= R.groups) return g;   // the second never holds for a plan
+            within -= n;
+            from = to;
+        }
     }
+};
+template <int TM>
+struct RowTiles {
+    __device__ __forceinline__ int operator()(const RouteRun& r) const { return (r.last - r.first + TM - 1) / TM; }
 };
 
 // ---------------------------------------------------------------------------
