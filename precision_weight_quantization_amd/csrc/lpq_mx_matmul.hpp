@@ -207,10 +207,13 @@ __device__ __forceinline__ void lds_arrived() { __asm__ volatile("s_waitcnt vmcn
 // L2 of its own: XCD x takes a run of tiles of its own, in columns of kTileGroup
 // rows of tiles, so that the workgroups that run on it at one time share few
 // rows of either operand.
-constexpr int kXcds = 8, kTileGroup = 8;
+// Routed rows: 2, for a group has few tiles of rows that share its b (8: 3% slower with 512 rows a group
+// on average, 1536 x 2048).
+constexpr int kXcds = 8, kTileGroup = 8, kRoutedTileGroup = 2;
+template <int GROUP>
 __device__ __forceinline__ void tile_at(int t, int tiles_n, int tiles_m, int& n, int& m) {
-    const int first = t / (kTileGroup * tiles_n) * kTileGroup;
-    const int rows = min(tiles_m - first, kTileGroup), in = t - first * tiles_n;
+    const int first = t / (GROUP * tiles_n) * GROUP;
+    const int rows = min(tiles_m - first, GROUP), in = t - first * tiles_n;
     m = first + in % rows;
     n = in / rows;
 }
@@ -293,8 +296,8 @@ __device__ __forceinline__ void mx_matmul_tiles(const MatmulArgs& A, int tiles_n
             const int g = cost.find(routing, at, r, within);
             return min(g * total + (int)((int64_t)within * total / cost.count(r)), total * routing.groups);
         };
-        run = border(xcd);
-        run_end = border(xcd + 1);
+        run = __builtin_amdgcn_readfirstlane(border(xcd));   // quotients are made in vector registers
+        run_end = __builtin_amdgcn_readfirstlane(border(xcd + 1));
     }
     const int slots = ((int)gridDim.x - xcd + kXcds - 1) / kXcds;
 
@@ -318,13 +321,14 @@ __device__ __forceinline__ void mx_matmul_tiles(const MatmulArgs& A, int tiles_n
         Tile t{};
         int n, m;
         if constexpr (MODE == ROUTED_K) {
-            t.group = tile / total;
+            t.group = __builtin_amdgcn_readfirstlane(tile / total);
             tile -= t.group * total;
             const RouteRun run = wave_run(routing, t.group);
             t.k = run.last / 32 * 32 - run.first / 32 * 32;   // whole blocks: a plan with align 32 has no others
             t.k0 = min(run.first / 32 * 32, A.K - 32);
         }
-        tile_at(tile, tiles_n, tiles_m, n, m);
+        tile_at<MODE == ROUTED_ROWS ? kRoutedTileGroup : kTileGroup>(tile, tiles_n, tiles_m, n, m);
+        if constexpr (MODE != DENSE) n = __builtin_amdgcn_readfirstlane(n), m = __builtin_amdgcn_readfirstlane(m);
         t.n0 = min((int64_t)n * TN, (int64_t)A.N - TN);
         if constexpr (MODE == ROUTED_ROWS) {
             RouteRun r;
@@ -552,12 +556,7 @@ __device__ __forceinline__ void mx_matmul_tiles(const MatmulArgs& A, int tiles_n
         if constexpr (MODE != DENSE)
             if (tile + slots < run_end) tile_next = tile_of(tile + slots);
         if constexpr (MODE == ROUTED_K) next_k = tile_next.k;
-        // A wave whose rows are all behind its group's last has no products to do: it helps with the loads only,
-        // and leaves the matrix cores to the others.
-        const int wave_row = tile_now.m0 + wm * FM * 16;
-        const bool busy = MODE != ROUTED_ROWS || (wave_row < tile_now.last && wave_row + FM * 16 > tile_now.first);
         for (int s = 0; s < steps; s++) {
-            if (busy)
             static_for<FN * KS - 1>([&](auto at) {
                 constexpr int x = decltype(at)::value, i = x % FN, ks = x / FN;
                 Frag<FP4B> next = fb[kAhead - 1];
@@ -593,12 +592,7 @@ __device__ __forceinline__ void mx_matmul_tiles(const MatmulArgs& A, int tiles_n
 #pragma unroll
             for (int i = 0; i < kAhead; i++) next[i] = frag_b(i, 0);
             const Scales next_sv = read_scales(0);
-            if (busy) {
-                products(std::integral_constant<int, FN - 1>{}, [&](int j) { fa[j] = frag_a(j, 0); });
-            } else {
-#pragma unroll
-                for (int j = 0; j < FM; j++) fa[j] = frag_a(j, 0);
-            }
+            products(std::integral_constant<int, FN - 1>{}, [&](int j) { fa[j] = frag_a(j, 0); });
             sv = next_sv;
 #pragma unroll
             for (int i = 0; i < kAhead; i++) fb[i] = next[i];
@@ -618,6 +612,9 @@ __device__ __forceinline__ void mx_matmul_tiles(const MatmulArgs& A, int tiles_n
         if constexpr (MODE == ROUTED_K) m0 += (int64_t)at.group * A.M;
         int N = A.N;   // opaque here: else the offsets of every store are formed before the first tile and kept
         __asm__ volatile("" : "+s"(N));
+        int lane = threadIdx.x & 63;   // opaque for the same reason, where registers are short
+        if constexpr (MODE != DENSE) __asm__ volatile("" : "+v"(lane));
+        const int g = lane >> 4, r = lane & 15;
         // Rows by way of LDS, 16 rows of 128 bytes at a time, so that 128 bytes of a row leave
         // in one piece: stored from the accumulators each instruction would write 32 bytes of
         // 16 rows (measured: 17 us of 233 at 8192 x 9728 x 2560).  Swizzled as a stage's rows

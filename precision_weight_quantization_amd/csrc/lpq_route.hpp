@@ -186,11 +186,11 @@ __device__ __forceinline__ int wave_scan(int v) {   // inclusive sums over the l
 template <typename Count>
 struct RouteMap {
     Count count;                    // of a run of rows
-    int share, upto, mine, total;   // groups a lane; counts up to and with its groups, of its groups; of all
+    int share, upto, total;   // groups a lane; count up to and with its groups; of all
     __device__ __forceinline__ RouteMap(const Routing& R, Count c) : count(c) {
         const int lane = threadIdx.x & 63;
         share = (R.groups + 63) / 64;
-        mine = 0;
+        int mine = 0;
         for (int i = 0; i < share; i++)
             if (lane * share + i < R.groups) mine += count(lane_run(R, lane * share + i));
         upto = wave_scan(mine);
@@ -199,7 +199,7 @@ struct RouteMap {
     // The group of place v < total, the same in every lane; its run, and the place within it.
     __device__ __forceinline__ int find(const Routing& R, int v, RouteRun& run, int& within) const {
         const int l = __builtin_ctzll(__builtin_amdgcn_ballot_w64(upto > v));
-        within = v - __builtin_amdgcn_readlane(upto - mine, l);
+        within = v - (l ? __builtin_amdgcn_readlane(upto, l ? l - 1 : 0) : 0);
         int g = l * share, from = wave_offset(R, g);
         for (;; g++) {
             const int to = wave_offset(R, g + 1);
