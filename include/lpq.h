@@ -642,6 +642,34 @@ lpq_status lpq_mx_matmul_routed_dw(const uint8_t* a, const uint8_t* ae, int a_fo
                                    int b_format, const int32_t* offsets, int32_t groups, int64_t M, int64_t N, int64_t capacity,
                                    void* y, int y_type, void* stream);
 
+/* Low-rank adapters of many requests at once, beside a shared projection (whose result is
+ * base): for token t of group g in a plan with one slot a token
+ *   y[t] = BF16(base[t] + scale[g] * (x[t] A[g]^T) B[g]^T)
+ * and y[t] = base[t] for a token without a row.  x: [tokens, K] BF16; A: [groups, rank, K],
+ * B: [groups, N, rank] BF16; scale: [groups] FP32, NULL: ones; base: [tokens, N] BF16, NULL:
+ * zeros, and may be y itself; offsets, rows [tokens], src [capacity]: the plan's (any align).  K, N and
+ * rank multiples of 8, rank up to 128, K and N up to 2^18, tokens and capacity up to 2^24, no
+ * matrix above 2^35 elements; arrays 16-byte aligned, scale and the plan's 4.  Sums are FP32, and so is u = x A^T in between, in an order fixed by the
+ * shape: a call's result does not vary.
+ * Backward, from dy [tokens, N], with u and du = scale * dy B computed again:
+ *   dx = BF16(dres + du A)    dres [tokens, K] BF16, NULL: zeros, and may be dx itself
+ *   dA[g] (+)= sum over the tokens of g of du^T x          [groups, rank, K] FP32
+ *   dB[g] (+)= sum over the tokens of g of scale * dy^T u   [groups, N, rank] FP32
+ * (added to what they hold when accumulate != 0; zeros for a group without tokens when it
+ * is 0).  The gradient of base is dy.  workspace: the bytes that
+ * lpq_adapters_workspace / lpq_adapters_backward_workspace say (less: LPQ_ERR_ARG; 0 for
+ * an invalid shape), 16-byte aligned, for this call alone while it runs.  Outputs overlap
+ * nothing else (LPQ_ERR_ARG). */
+int64_t lpq_adapters_workspace(int64_t tokens, int64_t capacity, int32_t groups, int32_t rank, int64_t N, int64_t K);
+lpq_status lpq_adapters(const uint16_t* x, const uint16_t* A, const uint16_t* B, const float* scale, const int32_t* offsets,
+                        const int32_t* rows, const int32_t* src, int64_t tokens, int64_t capacity, int32_t groups, int32_t rank,
+                        int64_t N, int64_t K, const uint16_t* base, uint16_t* y, void* workspace, int64_t workspace_bytes, void* stream);
+int64_t lpq_adapters_backward_workspace(int64_t tokens, int64_t capacity, int32_t groups, int32_t rank, int64_t N, int64_t K);
+lpq_status lpq_adapters_backward(const uint16_t* dy, const uint16_t* x, const uint16_t* A, const uint16_t* B, const float* scale,
+                                 const int32_t* offsets, const int32_t* rows, const int32_t* src, int64_t tokens, int64_t capacity,
+                                 int32_t groups, int32_t rank, int64_t N, int64_t K, const uint16_t* dres, uint16_t* dx, float* dA,
+                                 float* dB, int accumulate, void* workspace, int64_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

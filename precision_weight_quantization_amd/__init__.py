@@ -105,6 +105,10 @@ _SIG = {
     "lpq_route_combine_backward": (_int, [_vp, _vp, _i64, _i64, _vp, _vp, _i64, _i64, _vp, _vp, _vp, _vp]),
     "lpq_mx_matmul_routed": (_int, [_vp, _vp, _int, _vp, _vp, _int, _vp, _i32, _i64, _i64, _i64, _vp, _int, _vp]),
     "lpq_mx_matmul_routed_dw": (_int, [_vp, _vp, _int, _vp, _vp, _int, _vp, _i32, _i64, _i64, _i64, _vp, _int, _vp]),
+    "lpq_adapters_workspace": (_i64, [_i64, _i64, _i32, _i32, _i64, _i64]),
+    "lpq_adapters": (_int, [*[_vp] * 7, _i64, _i64, _i32, _i32, _i64, _i64, _vp, _vp, _vp, _i64, _vp]),
+    "lpq_adapters_backward_workspace": (_i64, [_i64, _i64, _i32, _i32, _i64, _i64]),
+    "lpq_adapters_backward": (_int, [*[_vp] * 8, _i64, _i64, _i32, _i32, _i64, _i64, _vp, _vp, _vp, _vp, _int, _vp, _i64, _vp]),
     "lpq_nvfp4_global_scale_reciprocal": (_int, [_vp, _i32, _vp, _vp]),
     "lpq_nvfp4_global_scale": (_int, [_vp, _i32, _vp, _vp]),
     "lpq_quantize_nvfp4_ex": (_int, [_vp, _i64, _i64, _vp, _int, _vp, _vp, _vp, _vp]),
@@ -1014,7 +1018,7 @@ def raw():
 
 # The calls of layers whose rows go to different weights (routed.py), found here under their C names.
 _ROUTED = ("lpq_route_capacity", "lpq_route_plan", "lpq_route_gather", "lpq_route_gather_mxfp8", "lpq_route_gather_mxfp4",
-           "lpq_mx_matmul_routed", "lpq_mx_matmul_routed_dw", "lpq_route_combine", "lpq_route_combine_backward")
+           "lpq_adapters", "lpq_adapters_backward", "lpq_mx_matmul_routed", "lpq_mx_matmul_routed_dw", "lpq_route_combine", "lpq_route_combine_backward")
 
 
 def __getattr__(name):

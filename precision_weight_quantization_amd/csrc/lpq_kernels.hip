@@ -59,6 +59,7 @@ using namespace lpq;
 #include "lpq_route.hpp"
 #include "lpq_mx_matmul.hpp"
 #include "lpq_mx_routed.hpp"
+#include "lpq_adapters.hpp"
 
 
 // ===========================================================================

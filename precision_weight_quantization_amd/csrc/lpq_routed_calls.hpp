@@ -167,9 +167,183 @@ lpq_status mx_matmul_routed_dw(const MatmulArgs& A, const Routing& R, hipStream_
     return L.template rows<2, 2, 1>();
 }
 
+// Adapters of one shape: x [tokens, K], y [tokens, N], factors of `rank`, rows in a plan.
+struct Adapters {
+    int64_t tokens, capacity;
+    int32_t groups, rank;
+    int64_t N, K;
+};
+// With these limits no launch below passes max_groups(), so that nothing is refused once a part is enqueued:
+// expand 2^22 workgroups of 256 threads (64 rows by 256 columns, 64 tokens to copy), gradient 2^22, transpose
+// 2^23, shrink 2^20 of 512.
+lpq_status adapters_shape(const Adapters& P) {
+    const int64_t most = int64_t(1) << 35;
+    if (P.groups <= 0 || P.groups > kRouteMaxGroups || P.rank <= 0 || P.rank > 128 || P.rank % 8) return LPQ_ERR_SHAPE;
+    if (P.N <= 0 || P.K <= 0 || P.N % 8 || P.K % 8 || P.tokens <= 0 || P.capacity <= 0) return LPQ_ERR_SHAPE;
+    if (P.N > (1 << 18) || P.K > (1 << 18) || P.tokens > (1 << 24) || P.capacity > (1 << 24)) return LPQ_ERR_SHAPE;
+    return P.tokens > most / P.N || P.tokens > most / P.K ? LPQ_ERR_SHAPE : LPQ_OK;
+}
+// Tiles of 16 * mt rows: at most, and about.
+int64_t adapter_tiles(const Adapters& P, int mt) { return P.capacity / (16 * mt) + (P.capacity < P.groups ? P.capacity : P.groups); }
+
+// The shrink's rows a workgroup: 32 where the accumulators of the rank's tiles leave room.
+int shrink_mt(const Adapters& P) { return P.rank <= 64 ? 2 : 1; }
+// Parts of its contraction: enough workgroups for the card, of 512 elements at least.
+int32_t shrink_splits(const Adapters& P, int64_t k) {
+    const int64_t groups = P.capacity < P.groups ? P.capacity : P.groups, tiles = ceil_div(P.capacity, 16 * shrink_mt(P));
+    int64_t s = 2 * kComputeUnits / (tiles > groups ? tiles : groups);
+    if (s > k / 512) s = k / 512;
+    return (int32_t)(s < 1 ? 1 : s > 16 ? 16 : s);
+}
+int64_t shrink_bytes(const Adapters& P, int64_t k) { return 4 * (int64_t)shrink_splits(P, k) * P.capacity * P.rank; }
+
+lpq_status adapter_shrink(const Adapters& P, const Routing& R, const uint16_t* x, const uint16_t* w, int64_t k, const int32_t* src,
+                          float* u, hipStream_t s) {
+    const int32_t splits = shrink_splits(P, k);
+    const ShrinkArgs A{x, w, src, u, P.tokens, (int32_t)k, P.rank, splits, (int32_t)(ceil_div(ceil_div(k, 32), splits) * 32)};
+    const int mt = shrink_mt(P), nt = (P.rank + 15) / 16;
+    const int64_t blocks = adapter_tiles(P, mt) * splits;
+    const dim3 grid((unsigned)blocks), block(64 * kShrinkWaves);
+    if (nt == 1) hipLaunchKernelGGL((k_adapter_shrink<1, 2>), grid, block, 0, s, A, R);
+    else if (nt == 2) hipLaunchKernelGGL((k_adapter_shrink<2, 2>), grid, block, 0, s, A, R);
+    else if (nt <= 4) hipLaunchKernelGGL((k_adapter_shrink<4, 2>), grid, block, 0, s, A, R);
+    else hipLaunchKernelGGL((k_adapter_shrink<8, 1>), grid, block, 0, s, A, R);
+    return launched();
+}
+
+// Columns of a wave of the expand: 256, less where that leaves the card idle.
+lpq_status adapter_expand(const Adapters& P, const Routing& R, const float* u, int32_t splits, const uint16_t* w, int64_t n,
+                          const float* scale, const int32_t* rows, const int32_t* src, const uint16_t* in, uint16_t* out, hipStream_t s) {
+    const int64_t copies = in == out ? 0 : ceil_div(P.tokens, 64), tiles = copies + adapter_tiles(P, 1);
+    int64_t columns = 256;
+    while (columns > 64 && ceil_div(tiles, kExpandWaves) * ceil_div(n, columns) < 4 * kComputeUnits) columns /= 2;
+    const int64_t chunks = ceil_div(n, columns), blocks = ceil_div(tiles, kExpandWaves) * chunks;
+    const ExpandArgs A{u, w, scale, rows, src, in, out, P.tokens, (int32_t)n, P.rank, splits, (int32_t)columns, (int32_t)chunks, (int32_t)copies};
+    const dim3 grid((unsigned)blocks), block(64 * kExpandWaves);
+    if (P.rank <= 32) hipLaunchKernelGGL(k_adapter_expand<1>, grid, block, 0, s, A, R);
+    else if (P.rank <= 64) hipLaunchKernelGGL(k_adapter_expand<2>, grid, block, 0, s, A, R);
+    else hipLaunchKernelGGL(k_adapter_expand<4>, grid, block, 0, s, A, R);
+    return launched();
+}
+
+// Parts of a group's rows in its gradients: enough workgroups for the card, of 128 rows at least.
+int32_t grad_splits(const Adapters& P, int64_t c) {
+    const int64_t wgs = ceil_div(c, 128) * ceil_div(P.rank, 64) * P.groups, most = ceil_div(P.capacity, 128);
+    int64_t s = 2 * kComputeUnits / wgs;
+    if (s > most) s = most;
+    return (int32_t)(s < 1 ? 1 : s > 32 ? 32 : s);
+}
+int64_t grad_bytes(const Adapters& P, int64_t c) {
+    const int32_t s = grad_splits(P, c);
+    return s == 1 ? 0 : 4 * (int64_t)s * P.groups * P.rank * c;
+}
+
+lpq_status adapter_grad(const Adapters& P, const Routing& R, const uint16_t* x, int64_t c, const float* v, int32_t parts,
+                        const float* scale, const int32_t* src, float* partial, float* out, int rank_last, int accumulate, hipStream_t s) {
+    const int32_t splits = grad_splits(P, c), tiles = (int32_t)ceil_div(c, 128), pieces = (int32_t)ceil_div(P.rank, 64);
+    const AdapterGradArgs A{x, v, scale, src, splits == 1 ? out : partial, P.tokens, (int32_t)c, P.rank, parts, splits, tiles, pieces,
+                            rank_last, splits == 1 ? accumulate : 0};
+    const int64_t blocks = (int64_t)tiles * pieces * P.groups * splits, n = (int64_t)P.groups * P.rank * c, sums = ceil_div(n, 1024);
+    const dim3 grid((unsigned)blocks), block(64 * kGradWaves);
+    if (P.rank <= 16) hipLaunchKernelGGL(k_adapter_grad<1>, grid, block, 0, s, A, R);
+    else if (P.rank <= 32) hipLaunchKernelGGL(k_adapter_grad<2>, grid, block, 0, s, A, R);
+    else hipLaunchKernelGGL(k_adapter_grad<4>, grid, block, 0, s, A, R);
+    const lpq_status st = launched();
+    if (st != LPQ_OK || splits == 1) return st;
+    hipLaunchKernelGGL(k_adapter_sum, dim3((unsigned)sums), dim3(256), 0, s, partial, out, n, splits, accumulate);
+    return launched();
+}
+
+lpq_status adapter_transpose(const uint16_t* in, uint16_t* out, int32_t groups, int64_t M, int64_t N, hipStream_t s) {
+    const AdapterTransposeArgs A{in, out, (int32_t)M, (int32_t)N, (int32_t)ceil_div(M, 64), (int32_t)ceil_div(N, 64)};
+    const int64_t blocks = (int64_t)groups * A.tiles_m * A.tiles_n;
+    hipLaunchKernelGGL(k_adapter_transpose, dim3((unsigned)blocks), dim3(256), 0, s, A);
+    return launched();
+}
+
+int64_t whole_lines(int64_t n) { return ceil_div(n, 256) * 256; }
+
 }  // namespace
 
 extern "C" {
+
+int64_t lpq_adapters_workspace(int64_t tokens, int64_t capacity, int32_t groups, int32_t rank, int64_t N, int64_t K) {
+    const Adapters P{tokens, capacity, groups, rank, N, K};
+    return adapters_shape(P) == LPQ_OK ? shrink_bytes(P, K) : 0;
+}
+
+lpq_status lpq_adapters(const uint16_t* x, const uint16_t* A, const uint16_t* B, const float* scale, const int32_t* offsets,
+                        const int32_t* rows, const int32_t* src, int64_t tokens, int64_t capacity, int32_t groups, int32_t rank,
+                        int64_t N, int64_t K, const uint16_t* base, uint16_t* y, void* workspace, int64_t workspace_bytes, void* stream) {
+    const Adapters P{tokens, capacity, groups, rank, N, K};
+    lpq_status st = adapters_shape(P);
+    if (st != LPQ_OK) return st;
+    if (!x || !A || !B || !offsets || !rows || !src || !y || !workspace) return LPQ_ERR_NULL;
+    if (!aligned(x, 16) || !aligned(A, 16) || !aligned(B, 16) || !aligned(base, 16) || !aligned(y, 16) || !aligned(workspace, 16) ||
+        !aligned(scale, 4) || !aligned(offsets, 4) || !aligned(rows, 4) || !aligned(src, 4))
+        return LPQ_ERR_ALIGN;
+    const int64_t need = shrink_bytes(P, K), factor = 2 * (int64_t)groups * rank;
+    if (workspace_bytes < need) return LPQ_ERR_ARG;
+    if (any_overlap({range(y, 2 * tokens * N), range(workspace, need)},
+                    {range(x, 2 * tokens * K), range(A, factor * K), range(B, factor * N), range(scale, 4 * groups),
+                     range(offsets, 4 * (groups + 1)), range(rows, 4 * tokens), range(src, 4 * capacity),
+                     range(base == y ? nullptr : base, 2 * tokens * N)}))
+        return LPQ_ERR_ARG;
+    const Routing R{offsets, groups, (int32_t)capacity};
+    const hipStream_t s = (hipStream_t)stream;
+    float* u = static_cast<float*>(workspace);
+    if ((st = adapter_shrink(P, R, x, A, K, src, u, s)) != LPQ_OK) return st;
+    return adapter_expand(P, R, u, shrink_splits(P, K), B, N, scale, rows, src, base, y, s);
+}
+
+int64_t lpq_adapters_backward_workspace(int64_t tokens, int64_t capacity, int32_t groups, int32_t rank, int64_t N, int64_t K) {
+    const Adapters P{tokens, capacity, groups, rank, N, K};
+    if (adapters_shape(P) != LPQ_OK) return 0;
+    const int64_t factor = 2 * (int64_t)groups * rank;
+    return whole_lines(factor * K) + whole_lines(factor * N) + whole_lines(shrink_bytes(P, K)) + whole_lines(shrink_bytes(P, N)) +
+           whole_lines(grad_bytes(P, K)) + grad_bytes(P, N);
+}
+
+lpq_status lpq_adapters_backward(const uint16_t* dy, const uint16_t* x, const uint16_t* A, const uint16_t* B, const float* scale,
+                                 const int32_t* offsets, const int32_t* rows, const int32_t* src, int64_t tokens, int64_t capacity,
+                                 int32_t groups, int32_t rank, int64_t N, int64_t K, const uint16_t* dres, uint16_t* dx, float* dA,
+                                 float* dB, int accumulate, void* workspace, int64_t workspace_bytes, void* stream) {
+    const Adapters P{tokens, capacity, groups, rank, N, K};
+    lpq_status st = adapters_shape(P);
+    if (st != LPQ_OK) return st;
+    if (!dy || !x || !A || !B || !offsets || !rows || !src || !dx || !dA || !dB || !workspace) return LPQ_ERR_NULL;
+    if (!aligned(dy, 16) || !aligned(x, 16) || !aligned(A, 16) || !aligned(B, 16) || !aligned(dres, 16) || !aligned(dx, 16) ||
+        !aligned(dA, 16) || !aligned(dB, 16) || !aligned(workspace, 16) || !aligned(scale, 4) || !aligned(offsets, 4) ||
+        !aligned(rows, 4) || !aligned(src, 4))
+        return LPQ_ERR_ALIGN;
+    const int64_t need = lpq_adapters_backward_workspace(tokens, capacity, groups, rank, N, K), factor = 2 * (int64_t)groups * rank;
+    if (workspace_bytes < need) return LPQ_ERR_ARG;
+    if (any_overlap({range(dx, 2 * tokens * K), range(dA, 2 * factor * K), range(dB, 2 * factor * N), range(workspace, need)},
+                    {range(dy, 2 * tokens * N), range(x, 2 * tokens * K), range(A, factor * K), range(B, factor * N),
+                     range(scale, 4 * groups), range(offsets, 4 * (groups + 1)), range(rows, 4 * tokens), range(src, 4 * capacity),
+                     range(dres == dx ? nullptr : dres, 2 * tokens * K)}))
+        return LPQ_ERR_ARG;
+    const Routing R{offsets, groups, (int32_t)capacity};
+    const hipStream_t s = (hipStream_t)stream;
+    uint8_t* at = static_cast<uint8_t*>(workspace);
+    auto take = [&](int64_t bytes) {
+        uint8_t* p = at;
+        at += whole_lines(bytes);
+        return p;
+    };
+    uint16_t* At = reinterpret_cast<uint16_t*>(take(factor * K));   // [groups, K, rank]
+    uint16_t* Bt = reinterpret_cast<uint16_t*>(take(factor * N));   // [groups, rank, N]
+    float* u = reinterpret_cast<float*>(take(shrink_bytes(P, K)));
+    float* du = reinterpret_cast<float*>(take(shrink_bytes(P, N)));
+    float* part_a = reinterpret_cast<float*>(take(grad_bytes(P, K)));
+    float* part_b = reinterpret_cast<float*>(at);
+    const int32_t parts = shrink_splits(P, K), dparts = shrink_splits(P, N);
+    if ((st = adapter_transpose(A, At, groups, rank, K, s)) != LPQ_OK || (st = adapter_transpose(B, Bt, groups, N, rank, s)) != LPQ_OK) return st;
+    if ((st = adapter_shrink(P, R, x, A, K, src, u, s)) != LPQ_OK || (st = adapter_shrink(P, R, dy, Bt, N, src, du, s)) != LPQ_OK) return st;
+    if ((st = adapter_grad(P, R, x, K, du, dparts, scale, src, part_a, dA, 0, accumulate, s)) != LPQ_OK) return st;
+    if ((st = adapter_grad(P, R, dy, N, u, parts, scale, src, part_b, dB, 1, accumulate, s)) != LPQ_OK) return st;
+    return adapter_expand(P, R, du, dparts, At, K, scale, rows, src, dres, dx, s);
+}
 
 lpq_status lpq_mx_matmul_routed(const uint8_t* a, const uint8_t* ae, int a_format, const uint8_t* b, const uint8_t* be, int b_format,
                                 const int32_t* offsets, int32_t groups, int64_t capacity, int64_t N, int64_t K, void* y, int y_type,

@@ -203,3 +203,69 @@ def lpq_route_combine_backward(dout, rows, src, weights=None, y=None, dy=None, d
             _ptr(y) if want_dweights else 0, R, N, rows.data_ptr(), src.data_ptr(), T, k, _ptr(weights), dy.data_ptr(),
             _ptr(dweights))
     return dy, dweights
+
+
+# --------------------------------------------------------------------------- adapters
+
+def _adapters(x, A, B, offsets, rows, src, scale):
+    """(tokens, capacity, groups, rank, N, K), every input checked."""
+    x = _bf16_in(x, "x")
+    T, K = x.shape
+    _arg(A, "A", x, dtypes=_p._BF16, dims=3)
+    _arg(B, "B", x, dtypes=_p._BF16, dims=3)
+    L, r, KA = A.shape
+    if KA != K or B.shape[0] != L or B.shape[2] != r:
+        raise ValueError(f"A must be [groups, rank, {K}] and B [groups, N, rank], got {tuple(A.shape)} and {tuple(B.shape)}")
+    if _offsets(offsets, x) != L:
+        raise ValueError(f"offsets is of {offsets.numel() - 1} groups, the adapters are {L}")
+    _, k = _tokens(rows, x, T)
+    if k != 1:
+        raise ValueError(f"a token has one adapter, the plan {k} slots a token")
+    R = _arg(src, "src", x, dtypes=_I32).numel()
+    if scale is not None:
+        _arg(scale, "scale", x, 4 * L, dtypes=(torch.float32,))
+    return T, R, L, r, B.shape[1], K
+
+
+def lpq_adapters(x, A, B, offsets, rows, src, scale=None, base=None, y=None, workspace=None, stream=None):
+    """y [tokens,N] = BF16(base + scale[g] (x A[g]^T) B[g]^T), g each token's adapter in a plan of one slot a token:
+    x [tokens,K], A [groups,rank,K], B [groups,N,rank] BF16 (K, N and rank multiples of 8, rank up to 128), scale
+    [groups] FP32 (None: ones), base [tokens,N] BF16 (None: zeros; ``y`` may be it)."""
+    T, R, L, r, N, K = dims = _adapters(x, A, B, offsets, rows, src, scale)
+    if base is not None:
+        _arg(base, "base", x, 2 * T * N, dtypes=_p._BF16)
+    need = _p._L.lpq_adapters_workspace(*dims)
+    if workspace is not None:
+        _arg(workspace, "workspace", x, need)
+    with _on(stream, x):
+        y, = _outs(x, (y, "y", 2 * T * N, (T, N), torch.bfloat16, 2))
+        if workspace is None:
+            workspace = _empty((need,), torch.uint8, x)
+    _launch(_p._L.lpq_adapters, "lpq_adapters", x, stream, x.data_ptr(), A.data_ptr(), B.data_ptr(), _ptr(scale),
+            offsets.data_ptr(), rows.data_ptr(), src.data_ptr(), *dims, _ptr(base), y.data_ptr(), workspace.data_ptr(),
+            workspace.numel() * workspace.element_size())
+    return y
+
+
+def lpq_adapters_backward(dy, x, A, B, offsets, rows, src, scale=None, dres=None, dx=None, dA=None, dB=None, accumulate=False,
+                          workspace=None, stream=None):
+    """Gradients of lpq_adapters from dy [tokens,N] BF16: (dx [tokens,K] BF16 = dres + ..., dA and dB like A and B in
+    FP32).  ``accumulate``: dA and dB, passed in, are added to."""
+    T, R, L, r, N, K = dims = _adapters(x, A, B, offsets, rows, src, scale)
+    _arg(dy, "dy", x, 2 * T * N, dtypes=_p._BF16)
+    if dres is not None:
+        _arg(dres, "dres", x, 2 * T * K, dtypes=_p._BF16)
+    if accumulate and (dA is None or dB is None):
+        raise ValueError("accumulate adds to the dA and dB that are passed in")
+    need = _p._L.lpq_adapters_backward_workspace(*dims)
+    if workspace is not None:
+        _arg(workspace, "workspace", x, need)
+    with _on(stream, x):
+        dx, dA, dB = _outs(x, (dx, "dx", 2 * T * K, (T, K), torch.bfloat16, 2), (dA, "dA", 4 * L * r * K, (L, r, K), torch.float32, 4),
+                           (dB, "dB", 4 * L * N * r, (L, N, r), torch.float32, 4))
+        if workspace is None:
+            workspace = _empty((need,), torch.uint8, x)
+    _launch(_p._L.lpq_adapters_backward, "lpq_adapters_backward", x, stream, dy.data_ptr(), x.data_ptr(), A.data_ptr(), B.data_ptr(),
+            _ptr(scale), offsets.data_ptr(), rows.data_ptr(), src.data_ptr(), *dims, _ptr(dres), dx.data_ptr(), dA.data_ptr(),
+            dB.data_ptr(), int(bool(accumulate)), workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    return dx, dA, dB

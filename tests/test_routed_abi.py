@@ -100,6 +100,32 @@ def test_product_refusals(lib):
     assert L.lpq_last_hip_error() == 0
 
 
+def test_adapter_refusals(lib):
+    L = lib.raw()
+    dims = dict(T=64, R=64, groups=3, rank=16, N=128, K=256)
+    W, WB = L.lpq_adapters_workspace, L.lpq_adapters_backward_workspace
+    need, back_need = W(*dims.values()), WB(*dims.values())
+    assert need >= 4 * 64 * 16 and back_need >= 2 * 3 * 16 * 384 + 8 * 64 * 16
+    bad = [dict(T=0), dict(R=0), dict(groups=0), dict(groups=1025), dict(rank=0), dict(rank=12), dict(rank=136), dict(N=0), dict(N=12), dict(K=0),
+           dict(K=20), dict(N=(1 << 18) + 8), dict(K=(1 << 18) + 8), dict(T=(1 << 24) + 1), dict(R=(1 << 24) + 1), dict(T=1 << 23, N=1 << 13)]
+    assert all(f(*{**dims, **c}.values()) == 0 for f in (W, WB) for c in bad)
+    call = caller(L.lpq_adapters, x=Q[0], A=Q[1], B=Q[2], scale=Q[3], off=Q[4], rows=Q[5], src=Q[6], **dims, base=Q[7], y=Q[8], ws=Q[9],
+                  bytes=need, stream=None)
+    back = caller(L.lpq_adapters_backward, dy=Q[10], x=Q[0], A=Q[1], B=Q[2], scale=Q[3], off=Q[4], rows=Q[5], src=Q[6], **dims, dres=Q[7],
+                  dx=Q[8], dA=Q[9], dB=Q[11], acc=0, ws=P + (12 << 24), bytes=back_need, stream=None)
+    refusals(call, 1, *({k: None} for k in ("x", "A", "B", "off", "rows", "src", "y", "ws")))
+    refusals(back, 1, *({k: None} for k in ("dy", "x", "A", "B", "off", "rows", "src", "dx", "dA", "dB", "ws")))
+    refusals(call, 2, *bad)
+    refusals(back, 2, *bad)
+    refusals(call, 3, *({k: Q[i] + 8} for k, i in (("x", 0), ("A", 1), ("B", 2), ("base", 7), ("y", 8), ("ws", 9))),
+             *({k: Q[i] + 2} for k, i in (("scale", 3), ("off", 4), ("rows", 5), ("src", 6))))
+    refusals(back, 3, *({k: Q[i] + 8} for k, i in (("dy", 10), ("x", 0), ("A", 1), ("B", 2), ("dres", 7), ("dx", 8), ("dA", 9), ("dB", 11))),
+             dict(ws=P + (12 << 24) + 8))
+    refusals(call, 6, dict(bytes=need - 1), dict(y=Q[0]), dict(y=Q[2]), dict(y=Q[7] + 16), dict(ws=Q[8]), dict(ws=Q[4]))
+    refusals(back, 6, dict(bytes=back_need - 1), dict(dx=Q[0]), dict(dx=Q[7] + 16), dict(dA=Q[1]), dict(dB=Q[9]), dict(dB=Q[10]), dict(ws=Q[6]))
+    assert L.lpq_last_hip_error() == 0
+
+
 def bf(*s):
     return fake(torch.zeros(s, dtype=torch.bfloat16))
 
@@ -168,6 +194,24 @@ def test_product_binding(lib, recorder):
     assert recorder.calls == []
 
 
+def test_adapter_binding(lib, recorder):
+    x, A, B, plan = bf(4, 64), bf(3, 8, 64), bf(3, 16, 8), (i32(4), i32(4), i32(4))
+    f = lib.lpq_adapters
+    refused([(TypeError, lambda: f(f32(4, 64), A, B, *plan)), (ValueError, lambda: f(x, bf(3, 8, 32), B, *plan)),
+             (ValueError, lambda: f(x, A, bf(2, 16, 8), *plan)), (ValueError, lambda: f(x, A, bf(3, 16, 16), *plan)),
+             (ValueError, lambda: f(x, bf(8, 64), B, *plan)), (ValueError, lambda: f(x, A, B, i32(5), i32(4), i32(4))),
+             (ValueError, lambda: f(x, A, B, i32(4), i32(3), i32(4))), (ValueError, lambda: f(x, A, B, i32(4), i32(4, 2), i32(8))),
+             (TypeError, lambda: f(x, A, B, i32(4), i32(4), f32(4))), (ValueError, lambda: f(x, A, B, *plan, scale=f32(2))),
+             (TypeError, lambda: f(x, A, B, *plan, scale=bf(3))), (ValueError, lambda: f(x, A, B, *plan, base=bf(4, 15))),
+             (ValueError, lambda: f(x, A, B, *plan, y=bf(3, 16)))])
+    f = lib.lpq_adapters_backward
+    dy = bf(4, 16)
+    refused([(ValueError, lambda: f(bf(4, 15), x, A, B, *plan)), (ValueError, lambda: f(dy, x, A, B, *plan, accumulate=True)),
+             (ValueError, lambda: f(dy, x, A, B, *plan, dres=bf(4, 63))), (ValueError, lambda: f(dy, x, A, B, *plan, dA=f32(3, 8, 63))),
+             (TypeError, lambda: f(dy, x, A, B, *plan, dB=bf(3, 16, 8))), (ValueError, lambda: f(dy, x, A, B, *plan, dx=bf(4, 63)))])
+    assert [c for c in recorder.calls if not c.endswith("_workspace")] == []
+
+
 # ----------------------------------------------------------------------------- device and stream
 
 def on1(dtype, *shape):
@@ -177,7 +221,11 @@ def on1(dtype, *shape):
 BF, U8, F32, I32 = torch.bfloat16, torch.uint8, torch.float32, torch.int32
 x, q, p, e, y = (lambda: on1(BF, 4, 64)), (lambda: on1(U8, 8, 64)), (lambda: on1(U8, 8, 32)), (lambda: on1(U8, 8, 2)), (lambda: on1(BF, 8, 64))
 rows, src, weights = (lambda: on1(I32, 4, 2)), (lambda: on1(I32, 8)), (lambda: on1(F32, 4, 2))
+AB = lambda: (on1(BF, 4, 8, 64), on1(BF, 4, 64, 8), on1(I32, 5), on1(I32, 4), on1(I32, 4))
 CALLS = {
+    "lpq_adapters": lambda **k: lpq.lpq_adapters(x(), *AB(), base=x(), y=x(), workspace=on1(U8, 64), **k),
+    "lpq_adapters_backward": lambda **k: lpq.lpq_adapters_backward(x(), x(), *AB(), dres=x(), dx=x(), dA=on1(F32, 4, 8, 64),
+                                                                   dB=on1(F32, 4, 64, 8), workspace=on1(U8, 64), **k),
     "lpq_route_plan": lambda **k: lpq.lpq_route_plan(rows(), 4, 1, on1(I32, 5), rows(), src(), **k),
     "lpq_route_gather": lambda **k: lpq.lpq_route_gather(x(), rows(), src(), y(), **k),
     "lpq_route_gather_mxfp8": lambda **k: lpq.lpq_route_gather_mxfp8(x(), rows(), src(), q(), e(), **k),
