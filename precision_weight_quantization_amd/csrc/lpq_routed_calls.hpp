@@ -197,33 +197,59 @@ int32_t shrink_splits(const Adapters& P, int64_t k) {
 }
 int64_t shrink_bytes(const Adapters& P, int64_t k) { return 4 * (int64_t)shrink_splits(P, k) * P.capacity * P.rank; }
 
-lpq_status adapter_shrink(const Adapters& P, const Routing& R, const uint16_t* x, const uint16_t* w, int64_t k, const int32_t* src,
-                          float* u, hipStream_t s) {
-    const int32_t splits = shrink_splits(P, k);
-    const ShrinkArgs A{x, w, src, u, P.tokens, (int32_t)k, P.rank, splits, (int32_t)(ceil_div(ceil_div(k, 32), splits) * 32)};
+struct Factor {
+    const uint16_t *x, *w;
+    float* u;
+    int64_t k;   // 0: none
+};
+lpq_status adapter_shrink(const Adapters& P, const Routing& R, const Factor& one, const Factor& two, const int32_t* src, hipStream_t s) {
     const int mt = shrink_mt(P), nt = (P.rank + 15) / 16;
-    const int64_t blocks = adapter_tiles(P, mt) * splits;
+    const int64_t tiles = adapter_tiles(P, mt);
+    ShrinkPair A{{}, src, P.tokens, P.rank};
+    int64_t blocks = 0;
+    for (int i = 0; i < 2; i++) {
+        const Factor& f = i ? two : one;
+        if (!f.k) continue;
+        const int32_t splits = shrink_splits(P, f.k);
+        A.a[i] = ShrinkArgs{f.x, f.w, f.u, (int32_t)f.k, splits, (int32_t)(ceil_div(ceil_div(f.k, 32), splits) * 32), (int32_t)(tiles * splits)};
+        blocks += tiles * splits;
+    }
     const dim3 grid((unsigned)blocks), block(64 * kShrinkWaves);
-    if (nt == 1) hipLaunchKernelGGL((k_adapter_shrink<1, 2>), grid, block, 0, s, A, R);
-    else if (nt == 2) hipLaunchKernelGGL((k_adapter_shrink<2, 2>), grid, block, 0, s, A, R);
-    else if (nt <= 4) hipLaunchKernelGGL((k_adapter_shrink<4, 2>), grid, block, 0, s, A, R);
-    else hipLaunchKernelGGL((k_adapter_shrink<8, 1>), grid, block, 0, s, A, R);
+    if (nt == 1) hipLaunchKernelGGL((k_adapter_shrink<1, 2, 4>), grid, block, 0, s, A, R);
+    else if (nt == 2) hipLaunchKernelGGL((k_adapter_shrink<2, 2, 4>), grid, block, 0, s, A, R);
+    else if (nt <= 4) hipLaunchKernelGGL((k_adapter_shrink<4, 2, 4>), grid, block, 0, s, A, R);
+    else hipLaunchKernelGGL((k_adapter_shrink<8, 1, 2>), grid, block, 0, s, A, R);
     return launched();
 }
 
-// Columns of a wave of the expand: 256, less where that leaves the card idle.
+// The expand's kernel: tiles of 64 rows where a group has as many on average; else 16 rows and 256
+// columns a wave, fewer columns where that leaves the card idle.
+template <int STEPS>
+lpq_status adapter_expand(ExpandArgs A, const Adapters& P, const Routing& R, hipStream_t s) {
+    const int64_t copies = A.in == A.out ? 0 : P.tokens;
+    if (P.capacity / P.groups >= 64) {
+        A.copy_tiles = (int32_t)ceil_div(copies, 64 * kExpandWaves);
+        A.chunks = (int32_t)ceil_div(A.N, kTileColumns);
+        hipLaunchKernelGGL(k_adapter_expand_tile<STEPS>, dim3((unsigned)((A.copy_tiles + adapter_tiles(P, 4)) * A.chunks)), dim3(64 * kExpandWaves),
+                           0, s, A, R);
+        return launched();
+    }
+    A.copy_tiles = (int32_t)ceil_div(copies, 64);
+    const int64_t tiles = A.copy_tiles + adapter_tiles(P, 1);
+    int64_t columns = 256;
+    while (columns > 64 && ceil_div(tiles, kExpandWaves) * ceil_div(A.N, columns) < 4 * kComputeUnits) columns /= 2;
+    A.chunks = (int32_t)ceil_div(A.N, columns);
+    const dim3 grid((unsigned)(ceil_div(tiles, kExpandWaves) * A.chunks)), block(64 * kExpandWaves);
+    if (columns == 256) hipLaunchKernelGGL((k_adapter_expand<STEPS, 4>), grid, block, 0, s, A, R);
+    else if (columns == 128) hipLaunchKernelGGL((k_adapter_expand<STEPS, 2>), grid, block, 0, s, A, R);
+    else hipLaunchKernelGGL((k_adapter_expand<STEPS, 1>), grid, block, 0, s, A, R);
+    return launched();
+}
 lpq_status adapter_expand(const Adapters& P, const Routing& R, const float* u, int32_t splits, const uint16_t* w, int64_t n,
                           const float* scale, const int32_t* rows, const int32_t* src, const uint16_t* in, uint16_t* out, hipStream_t s) {
-    const int64_t copies = in == out ? 0 : ceil_div(P.tokens, 64), tiles = copies + adapter_tiles(P, 1);
-    int64_t columns = 256;
-    while (columns > 64 && ceil_div(tiles, kExpandWaves) * ceil_div(n, columns) < 4 * kComputeUnits) columns /= 2;
-    const int64_t chunks = ceil_div(n, columns), blocks = ceil_div(tiles, kExpandWaves) * chunks;
-    const ExpandArgs A{u, w, scale, rows, src, in, out, P.tokens, (int32_t)n, P.rank, splits, (int32_t)columns, (int32_t)chunks, (int32_t)copies};
-    const dim3 grid((unsigned)blocks), block(64 * kExpandWaves);
-    if (P.rank <= 32) hipLaunchKernelGGL(k_adapter_expand<1>, grid, block, 0, s, A, R);
-    else if (P.rank <= 64) hipLaunchKernelGGL(k_adapter_expand<2>, grid, block, 0, s, A, R);
-    else hipLaunchKernelGGL(k_adapter_expand<4>, grid, block, 0, s, A, R);
-    return launched();
+    const ExpandArgs A{u, w, scale, rows, src, in, out, P.tokens, (int32_t)n, P.rank, splits, 0, 0};
+    if (P.rank <= 32) return adapter_expand<1>(A, P, R, s);
+    return P.rank <= 64 ? adapter_expand<2>(A, P, R, s) : adapter_expand<4>(A, P, R, s);
 }
 
 // Parts of a group's rows in its gradients: enough workgroups for the card, of 128 rows at least.
@@ -237,27 +263,54 @@ int64_t grad_bytes(const Adapters& P, int64_t c) {
     const int32_t s = grad_splits(P, c);
     return s == 1 ? 0 : 4 * (int64_t)s * P.groups * P.rank * c;
 }
+int64_t planes_pitch(const Adapters& P) { return ceil_div(P.capacity + 32, 64) * 64; }   // a step may pass the rows by 31
+int64_t planes_bytes(const Adapters& P) { return 3 * 2 * P.rank * planes_pitch(P); }
 
-lpq_status adapter_grad(const Adapters& P, const Routing& R, const uint16_t* x, int64_t c, const float* v, int32_t parts,
-                        const float* scale, const int32_t* src, float* partial, float* out, int rank_last, int accumulate, hipStream_t s) {
-    const int32_t splits = grad_splits(P, c), tiles = (int32_t)ceil_div(c, 128), pieces = (int32_t)ceil_div(P.rank, 64);
-    const AdapterGradArgs A{x, v, scale, src, splits == 1 ? out : partial, P.tokens, (int32_t)c, P.rank, parts, splits, tiles, pieces,
-                            rank_last, splits == 1 ? accumulate : 0};
-    const int64_t blocks = (int64_t)tiles * pieces * P.groups * splits, n = (int64_t)P.groups * P.rank * c, sums = ceil_div(n, 1024);
+struct Gradient {
+    const uint16_t* x;
+    int64_t c;
+    const uint16_t* planes;
+    float *partial, *out;
+    int rank_last;
+};
+lpq_status adapter_grad(const Adapters& P, const Routing& R, const Gradient (&g)[2], const float* scale, const int32_t* src,
+                        int accumulate, hipStream_t s) {
+    const int32_t pieces = (int32_t)ceil_div(P.rank, 64);
+    AdapterGradPair A{{}, scale, src, P.tokens, P.rank, (int32_t)planes_pitch(P), pieces};
+    AdapterSumArgs sum{};
+    int64_t blocks = 0, sums = 0;
+    for (int i = 0; i < 2; i++) {
+        const int32_t splits = grad_splits(P, g[i].c), tiles = (int32_t)ceil_div(g[i].c, 128);
+        const int64_t here = (int64_t)tiles * pieces * P.groups * splits, n = (int64_t)P.groups * P.rank * g[i].c;
+        A.a[i] = AdapterGradArgs{g[i].x, g[i].planes, splits == 1 ? g[i].out : g[i].partial, (int32_t)g[i].c, splits, tiles, g[i].rank_last,
+                                 splits == 1 ? accumulate : 0, (int32_t)here};
+        blocks += here;
+        sum.in[i] = g[i].partial;
+        sum.out[i] = g[i].out;
+        sum.n[i] = splits == 1 ? 0 : n;
+        sum.parts[i] = splits;
+        if (splits > 1) sums += ceil_div(n, 1024);
+        if (i == 0) sum.blocks = (int32_t)sums;
+    }
+    sum.accumulate = accumulate;
     const dim3 grid((unsigned)blocks), block(64 * kGradWaves);
     if (P.rank <= 16) hipLaunchKernelGGL(k_adapter_grad<1>, grid, block, 0, s, A, R);
     else if (P.rank <= 32) hipLaunchKernelGGL(k_adapter_grad<2>, grid, block, 0, s, A, R);
     else hipLaunchKernelGGL(k_adapter_grad<4>, grid, block, 0, s, A, R);
     const lpq_status st = launched();
-    if (st != LPQ_OK || splits == 1) return st;
-    hipLaunchKernelGGL(k_adapter_sum, dim3((unsigned)sums), dim3(256), 0, s, partial, out, n, splits, accumulate);
+    if (st != LPQ_OK || sums == 0) return st;
+    hipLaunchKernelGGL(k_adapter_sum, dim3((unsigned)sums), dim3(256), 0, s, sum);
     return launched();
 }
 
-lpq_status adapter_transpose(const uint16_t* in, uint16_t* out, int32_t groups, int64_t M, int64_t N, hipStream_t s) {
-    const AdapterTransposeArgs A{in, out, (int32_t)M, (int32_t)N, (int32_t)ceil_div(M, 64), (int32_t)ceil_div(N, 64)};
-    const int64_t blocks = (int64_t)groups * A.tiles_m * A.tiles_n;
-    hipLaunchKernelGGL(k_adapter_transpose, dim3((unsigned)blocks), dim3(256), 0, s, A);
+// A^T and B^T.
+lpq_status adapter_transpose(const Adapters& P, const uint16_t* A, uint16_t* At, const uint16_t* B, uint16_t* Bt, hipStream_t s) {
+    auto one = [&](const uint16_t* in, uint16_t* out, int64_t m, int64_t n) {
+        const int32_t tm = (int32_t)ceil_div(m, 64), tn = (int32_t)ceil_div(n, 64);
+        return AdapterTransposeArgs{in, out, (int32_t)m, (int32_t)n, tm, tn, P.groups * tm * tn};
+    };
+    const AdapterTransposePair T{{one(A, At, P.rank, P.K), one(B, Bt, P.N, P.rank)}};
+    hipLaunchKernelGGL(k_adapter_transpose, dim3((unsigned)(T.a[0].blocks + T.a[1].blocks)), dim3(256), 0, s, T);
     return launched();
 }
 
@@ -292,7 +345,7 @@ lpq_status lpq_adapters(const uint16_t* x, const uint16_t* A, const uint16_t* B,
     const Routing R{offsets, groups, (int32_t)capacity};
     const hipStream_t s = (hipStream_t)stream;
     float* u = static_cast<float*>(workspace);
-    if ((st = adapter_shrink(P, R, x, A, K, src, u, s)) != LPQ_OK) return st;
+    if ((st = adapter_shrink(P, R, {x, A, u, K}, {}, src, s)) != LPQ_OK) return st;
     return adapter_expand(P, R, u, shrink_splits(P, K), B, N, scale, rows, src, base, y, s);
 }
 
@@ -301,7 +354,7 @@ int64_t lpq_adapters_backward_workspace(int64_t tokens, int64_t capacity, int32_
     if (adapters_shape(P) != LPQ_OK) return 0;
     const int64_t factor = 2 * (int64_t)groups * rank;
     return whole_lines(factor * K) + whole_lines(factor * N) + whole_lines(shrink_bytes(P, K)) + whole_lines(shrink_bytes(P, N)) +
-           whole_lines(grad_bytes(P, K)) + grad_bytes(P, N);
+           2 * whole_lines(planes_bytes(P)) + whole_lines(grad_bytes(P, K)) + grad_bytes(P, N);
 }
 
 lpq_status lpq_adapters_backward(const uint16_t* dy, const uint16_t* x, const uint16_t* A, const uint16_t* B, const float* scale,
@@ -335,13 +388,17 @@ lpq_status lpq_adapters_backward(const uint16_t* dy, const uint16_t* x, const ui
     uint16_t* Bt = reinterpret_cast<uint16_t*>(take(factor * N));   // [groups, rank, N]
     float* u = reinterpret_cast<float*>(take(shrink_bytes(P, K)));
     float* du = reinterpret_cast<float*>(take(shrink_bytes(P, N)));
+    uint16_t* planes[2] = {reinterpret_cast<uint16_t*>(take(planes_bytes(P))), reinterpret_cast<uint16_t*>(take(planes_bytes(P)))};
     float* part_a = reinterpret_cast<float*>(take(grad_bytes(P, K)));
     float* part_b = reinterpret_cast<float*>(at);
     const int32_t parts = shrink_splits(P, K), dparts = shrink_splits(P, N);
-    if ((st = adapter_transpose(A, At, groups, rank, K, s)) != LPQ_OK || (st = adapter_transpose(B, Bt, groups, N, rank, s)) != LPQ_OK) return st;
-    if ((st = adapter_shrink(P, R, x, A, K, src, u, s)) != LPQ_OK || (st = adapter_shrink(P, R, dy, Bt, N, src, du, s)) != LPQ_OK) return st;
-    if ((st = adapter_grad(P, R, x, K, du, dparts, scale, src, part_a, dA, 0, accumulate, s)) != LPQ_OK) return st;
-    if ((st = adapter_grad(P, R, dy, N, u, parts, scale, src, part_b, dB, 1, accumulate, s)) != LPQ_OK) return st;
+    if ((st = adapter_transpose(P, A, At, B, Bt, s)) != LPQ_OK) return st;
+    if ((st = adapter_shrink(P, R, {x, A, u, K}, {dy, Bt, du, N}, src, s)) != LPQ_OK) return st;
+    const AdapterPlanesArgs planes_args{{du, u}, {planes[0], planes[1]}, {dparts, parts}, rank, (int32_t)planes_pitch(P)};
+    hipLaunchKernelGGL(k_adapter_planes, dim3((unsigned)(planes_pitch(P) / 64), (unsigned)ceil_div(rank, 16), 2), dim3(256), 0, s, planes_args, R);
+    if ((st = launched()) != LPQ_OK) return st;
+    const Gradient gradients[2] = {{x, K, planes[0], part_a, dA, 0}, {dy, N, planes[1], part_b, dB, 1}};
+    if ((st = adapter_grad(P, R, gradients, scale, src, accumulate, s)) != LPQ_OK) return st;
     return adapter_expand(P, R, du, dparts, At, K, scale, rows, src, dres, dx, s);
 }
 
