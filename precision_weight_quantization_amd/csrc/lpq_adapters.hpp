@@ -95,8 +95,9 @@ __global__ __launch_bounds__(64 * kShrinkWaves) void k_adapter_shrink(ShrinkPair
 #pragma unroll
         for (int i = 0; i < MT; i++) c[j][i] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
     }
-    const int begin = split * A.each, end = min(begin + A.each, A.K);
-    for (int k0 = begin + wave * 32 * U; k0 < end; k0 += W * 32 * U) {
+    const int steps = (min(A.each, A.K - split * A.each) + 31) / 32, share = (steps + W - 1) / W;
+    const int begin = split * A.each + wave * share * 32, end = min(min(begin + share * 32, split * A.each + A.each), A.K);
+    for (int k0 = begin; k0 < end; k0 += 32 * U) {
         v4u fx[U][MT], fw[U][NT];
 #pragma unroll
         for (int u = 0; u < U; u++) {

@@ -620,6 +620,20 @@ __device__ __forceinline__ void mx_matmul_tiles(const MatmulArgs& A, int tiles_n
         // 16 rows (measured: 17 us of 233 at 8192 x 9728 x 2560).  Swizzled as a stage's rows
         // are.  Non-temporal: 9 us of 207 there; but not in parts of lines, which then are
         // joined in memory (96 results of 520 x 776 in FP32: 133 us and 54).
+        auto put_rows = [&](auto f32, uint8_t* mine, int j, int h) {   // 128 bytes of 16 rows
+            constexpr bool F32 = decltype(f32)::value;
+            constexpr int kFrags = F32 ? 2 : 4;   // 16-column results in 128 bytes
+#pragma unroll
+            for (int i = 0; i < kFrags; i++) {
+                const v4f v = c[h + i][j];
+                if constexpr (F32)
+                    *reinterpret_cast<v4f*>(mine + r * 128 + ((i * 4 + g) ^ ((r >> 1) & 7)) * 16) = v;
+                else
+                    *reinterpret_cast<v2u*>(mine + r * 128 + ((i * 2 + (g >> 1)) ^ ((r >> 1) & 7)) * 16 + (g & 1) * 8) =
+                        v2u{bf16x2(v[0], v[1]), bf16x2(v[2], v[3])};
+            }
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        };
         auto store_rows = [&](auto f32, auto nt) {
             constexpr bool F32 = decltype(f32)::value;
             constexpr int kSize = F32 ? 4 : 2, kFrags = F32 ? 2 : 4;   // 16-column results in 128 bytes
@@ -630,16 +644,7 @@ __device__ __forceinline__ void mx_matmul_tiles(const MatmulArgs& A, int tiles_n
             for (int j = 0; j < FM; j++) {
 #pragma unroll
                 for (int h = 0; h < FN; h += kFrags) {
-#pragma unroll
-                    for (int i = 0; i < kFrags; i++) {
-                        const v4f v = c[h + i][j];
-                        if constexpr (F32)
-                            *reinterpret_cast<v4f*>(mine + r * 128 + ((i * 4 + g) ^ ((r >> 1) & 7)) * 16) = v;
-                        else
-                            *reinterpret_cast<v2u*>(mine + r * 128 + ((i * 2 + (g >> 1)) ^ ((r >> 1) & 7)) * 16 + (g & 1) * 8) =
-                                v2u{bf16x2(v[0], v[1]), bf16x2(v[2], v[3])};
-                    }
-                    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+                    put_rows(f32, mine, j, h);
 #pragma unroll
                     for (int x = 0; x < 16; x += 8) {
                         const int row = x + (lane >> 3);
@@ -652,7 +657,7 @@ __device__ __forceinline__ void mx_matmul_tiles(const MatmulArgs& A, int tiles_n
                 }
             }
         };
-        if (A.f32 ? N % 4 == 0 : N % 8 == 0) {
+        if ((MODE != DENSE && TN == 256) || (A.f32 ? N % 4 == 0 : N % 8 == 0)) {
             if (whole_lines) {
                 if (A.f32) store_rows(std::true_type{}, std::true_type{});
                 else store_rows(std::false_type{}, std::true_type{});
@@ -660,6 +665,33 @@ __device__ __forceinline__ void mx_matmul_tiles(const MatmulArgs& A, int tiles_n
                 if (A.f32) store_rows(std::true_type{}, std::false_type{});
                 else store_rows(std::false_type{}, std::false_type{});
             }
+        } else if constexpr (MODE != DENSE) {
+            // Rows that no vector divides (128 x 128 tiles only): by way of LDS too, then element by element along a row
+            // (from the accumulators, one element of 16 rows by 4 columns at a time: 30 us instead of 20 for
+            // 4206 rows of 60 groups, 1021 x 1056, MXFP4 with an FP32 result).
+            auto store_elements = [&](auto f32) {
+                constexpr bool F32 = decltype(f32)::value;
+                constexpr int kSize = F32 ? 4 : 2, kFrags = F32 ? 2 : 4, kCols = 16 * kFrags;
+                using E = std::conditional_t<F32, float, uint16_t>;
+                uint8_t* mine = lds + kOut + wave * 2048;
+                E* y = static_cast<E*>(A.y) + (m0 * N + n0);   // uniform
+                const int col = lane % kCols;
+#pragma unroll
+                for (int j = 0; j < FM; j++) {
+                    if (MODE == ROUTED_ROWS && (row_first >= j * 16 + 16 || row_last <= j * 16)) continue;
+#pragma unroll
+                    for (int h = 0; h < FN; h += kFrags) {
+                        put_rows(f32, mine, j, h);
+                        for (int x = lane / kCols; x < 16; x += 64 / kCols) {
+                            const E v = *reinterpret_cast<const E*>(mine + x * 128 + ((col * kSize / 16) ^ ((x >> 1) & 7)) * 16 + col * kSize % 16);
+                            if (keeps(j * 16 + x)) store<false>(y + (uint32_t)((j * 16 + x) * N + h * 16 + col), v);
+                        }
+                        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+                    }
+                }
+            };
+            if (A.f32) store_elements(std::true_type{});
+            else store_elements(std::false_type{});
         } else {
             uint8_t* y = static_cast<uint8_t*>(A.y) + (m0 * N + n0) * (A.f32 ? 4 : 2);
 #pragma unroll

@@ -8,16 +8,19 @@
 
 namespace {
 
-// ROUTED_ROWS: y[r] = a[r] b[group of r]^T, a workgroup takes up to 16 * MT rows of
-// one group and 16 * NT rows of its b.  ROUTED_K: y[g] = a[:, rows of g] b[:, rows
-// of g]^T, 16 * MT rows of a, 16 * NT of b.  As in k_mx_matmul_rows the waves share
-// out k in steps of 128 and add their results through LDS.
-template <bool FP4B, bool FP4A, int NT, int MT, int U, TileMode MODE>
+// ROUTED_ROWS: y[r] = a[r] b[group of r]^T, for up to 16 * MT rows of one group and 16 * NT
+// rows of its b.  ROUTED_K: y[g] = a[:, rows of g] b[:, rows of g]^T, 16 * MT rows of a, 16 * NT
+// of b.  W waves share out k in steps of 128 and add their results through LDS; a
+// workgroup holds 8 / W such tiles side by side, because a wave of few steps spends its time
+// on finding its group and on one round trip to memory.
+template <bool FP4B, bool FP4A, int NT, int MT, int U, int W, TileMode MODE>
 __global__ __launch_bounds__(64 * kRowsWaves) void k_mx_matmul_routed_rows(MatmulArgs A, int tiles_n, int tiles_m, Routing routing,
                                                                            int first) {
-    constexpr int W = kRowsWaves;
-    __shared__ v4f part[W][NT * MT][64];
-    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, g = lane >> 4, r = lane & 15;
+    constexpr int C = kRowsWaves / W;   // column tiles of the workgroup
+    __shared__ v4f parts[C][W][NT * MT][64];
+    const int lane = threadIdx.x & 63, g = lane >> 4, r = lane & 15;
+    const int wave = (threadIdx.x >> 6) % W, column = (threadIdx.x >> 6) / W;
+    auto& part = parts[column];
     int tile = first + (int)blockIdx.x, group, k0 = 0, K = A.K;
     int64_t m_first, m_last;
     if constexpr (MODE == ROUTED_ROWS) {
@@ -38,7 +41,7 @@ __global__ __launch_bounds__(64 * kRowsWaves) void k_mx_matmul_routed_rows(Matmu
         m_first = (int64_t)(tile / tiles_n) * 16 * MT;
         m_last = A.M;
     }
-    const int64_t n_first = (int64_t)(tile % tiles_n) * 16 * NT, b_first = MODE == ROUTED_ROWS ? (int64_t)group * A.N : 0;
+    const int64_t n_first = ((int64_t)(tile % tiles_n) * C + column) * 16 * NT, b_first = MODE == ROUTED_ROWS ? (int64_t)group * A.N : 0;
     const uint8_t *a[MT], *ae[MT], *b[NT], *be[NT];
     bool in_m[MT], in_n[NT];
     v4f c[NT][MT];

@@ -116,14 +116,14 @@ struct RoutedLaunch {
         const int64_t most = R.capacity < R.groups ? R.capacity : R.groups;
         return R.capacity / tm + most;
     }
-    template <int NT, int MT, int U>
+    template <int NT, int MT, int U, int W>
     lpq_status rows() const {
-        const int64_t tiles_n = ceil_div(A.N, 16 * NT), tiles_m = MODE == ROUTED_K ? ceil_div(A.M, 16 * MT) : 1;
+        const int64_t tiles_n = ceil_div(A.N, 16 * NT * (kRowsWaves / W)), tiles_m = MODE == ROUTED_K ? ceil_div(A.M, 16 * MT) : 1;
         const int64_t tiles = MODE == ROUTED_K ? tiles_n * tiles_m * R.groups : tiles_n * row_tiles(16 * MT);
         const int64_t most = max_groups(64 * kRowsWaves);
         if (tiles > 0x7fffffffLL) return LPQ_ERR_SHAPE;   // tile indexes are 32-bit
         for (int64_t first = 0; first < tiles; first += most) {
-            hipLaunchKernelGGL((k_mx_matmul_routed_rows<FP4B, FP4A, NT, MT, U, MODE>),
+            hipLaunchKernelGGL((k_mx_matmul_routed_rows<FP4B, FP4A, NT, MT, U, W, MODE>),
                                dim3((unsigned)(tiles - first < most ? tiles - first : most)), dim3(64 * kRowsWaves), 0, s, A,
                                (int)tiles_n, (int)tiles_m, R, (int)first);
             const lpq_status st = launched();
@@ -143,17 +143,39 @@ struct RoutedLaunch {
     }
 };
 
+// Rows of y in vectors of 16 bytes, which the large tiles store.
+bool whole_vectors(const MatmulArgs& A) { return A.f32 ? A.N % 4 == 0 : A.N % 8 == 0; }
+
+// Which kernel, by the rows that a group has on average (the counts themselves are on the device).  Both
+// sides were timed with k = 2048 or 768, N = 1536 or 2048, 128 groups, MXFP8 unless said, rows drawn at random; us:
+//  * Tiles by way of LDS from 24 rows on: 19 rows 133 in tiles, 110 by rows; 25 rows 54 and 59 (k = 768);
+//    37 rows 97 and 142; 56 rows 93 and 177.  A tile's stages take as long as its weights, whatever its rows.
+//  * 256 x 256 from 144 rows on: 75 rows 130 against 101 with 128 x 128, 125 rows 108 and 102 (MXFP4 weights), 150
+//    rows 123 and 149, 200 rows 134 and 157; 250 rows 186 and 178, where most groups just need a second tile.
+//  * Rows: 16 rows a tile up to 16 on average, 32 above.  Columns of a wave: as many as leave a few waves for each
+//    SIMD (1 token of 8 experts, N = 2048, k = 768, MXFP4 weights: 4.7 with 16 columns, 5.6 with 32, 7.8 with 64; 24
+//    tokens 31, 27 and 25).
+//    Waves that share out k: of 3 steps at least (24 tokens, N = 2048, k = 768: 37 with 8, 31 with 2, 27 with 1;
+//    4 tokens, N = 4096, k = 7168: 167 with 8, 179 with 4).
 template <bool FP4A, bool FP4B>
 lpq_status mx_matmul_routed(const MatmulArgs& A, const Routing& R, hipStream_t s) {
     const RoutedLaunch<FP4A, FP4B, ROUTED_ROWS> L{A, R, s};
     const int64_t average = R.capacity / R.groups;
     const bool limits = A.K > 128 * stage_steps<FP4B, FP4A>() && A.K <= (1 << 22) && A.N <= (1 << 22);
-    if (limits && average >= 64 && A.N >= 128 && R.capacity >= 128) {
-        if (average >= 192 && A.N >= 256 && R.capacity >= 256) return L.template tile<256, 256, 2, 4>();
+    if (limits && average >= 24 && A.N >= 128 && R.capacity >= 128) {
+        if (average >= 144 && A.N >= 256 && whole_vectors(A) && R.capacity >= 256) return L.template tile<256, 256, 2, 4>();
         return L.template tile<128, 128, 2, 2>();
     }
-    if (average <= 16) return L.template rows<1, 1, 1>();
-    return average <= 32 ? L.template rows<2, 2, 1>() : L.template rows<2, 4, 1>();
+    const int64_t steps = ceil_div(A.K, 128), tiles = L.row_tiles(16) * ceil_div(A.N, 64);
+    auto by_share = [&](auto nt, auto mt, auto u) {
+        constexpr int NT = decltype(nt)::value, MT = decltype(mt)::value, U = decltype(u)::value;
+        if (steps >= 24) return L.template rows<NT, MT, U, 8>();
+        if (steps >= 12) return L.template rows<NT, MT, U, 4>();
+        return steps >= 6 ? L.template rows<NT, MT, U, 2>() : L.template rows<NT, MT, U, 1>();
+    };
+    if (average > 16) return by_share(Int<4>{}, Int<2>{}, Int<1>{});   // 19 rows: 110, and 128 with 32 columns
+    if (tiles > 2048 && steps < 24) return by_share(Int<4>{}, Int<1>{}, Int<1>{});
+    return tiles > 512 ? by_share(Int<2>{}, Int<1>{}, Int<3>{}) : by_share(Int<1>{}, Int<1>{}, Int<3>{});
 }
 
 template <bool FP4A, bool FP4B>
@@ -161,10 +183,10 @@ lpq_status mx_matmul_routed_dw(const MatmulArgs& A, const Routing& R, hipStream_
     const RoutedLaunch<FP4A, FP4B, ROUTED_K> L{A, R, s};
     const bool limits = A.K <= (1 << 22) && A.N <= (1 << 22);
     if (limits && A.M >= 128 && A.N >= 128) {
-        if (A.M >= 256 && A.N >= 256) return L.template tile<256, 256, 2, 4>();
+        if (A.M >= 256 && A.N >= 256 && whole_vectors(A)) return L.template tile<256, 256, 2, 4>();
         return L.template tile<128, 128, 2, 2>();
     }
-    return L.template rows<2, 2, 1>();
+    return L.template rows<2, 2, 1, 4>();
 }
 
 // Adapters of one shape: x [tokens, K], y [tokens, N], factors of `rank`, rows in a plan.
@@ -191,7 +213,7 @@ int shrink_mt(const Adapters& P) { return P.rank <= 64 ? 2 : 1; }
 // Parts of its contraction: enough workgroups for the card, of 512 elements at least.
 int32_t shrink_splits(const Adapters& P, int64_t k) {
     const int64_t groups = P.capacity < P.groups ? P.capacity : P.groups, tiles = ceil_div(P.capacity, 16 * shrink_mt(P));
-    int64_t s = 2 * kComputeUnits / (tiles > groups ? tiles : groups);
+    int64_t s = kComputeUnits / (tiles > groups ? tiles : groups);
     if (s > k / 512) s = k / 512;
     return (int32_t)(s < 1 ? 1 : s > 16 ? 16 : s);
 }
