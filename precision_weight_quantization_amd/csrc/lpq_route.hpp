@@ -234,17 +234,19 @@ __device__ __forceinline__ TokenVec token_vec(int64_t block, int64_t tokens, int
     return {token + more, (int)(in_row - more * vecs) * 8, token + more < tokens};
 }
 
-// Rows without a pair: a wave looks at 64 of them and calls zero(row) with all its
-// lanes for each.
+// Rows without a pair: a workgroup looks at kPadRows of them and calls zero(row) with all its
+// threads for each (a wave by itself for 64 rows: 62 us instead of 45 where 5,700 of 9,400
+// rows of 14 KB are empty, the last waves').
+constexpr int kPadRows = 16;
 template <typename F>
 __device__ __forceinline__ void zero_rows(const int32_t* src, int64_t capacity, F&& zero) {
     const int lane = threadIdx.x & 63;
-    const int64_t r0 = ((int64_t)blockIdx.x * (blockDim.x / 64) + (threadIdx.x >> 6)) * 64;
-    const bool empty = r0 + lane < capacity && src[r0 + lane] < 0;
-    for (uint64_t m = __builtin_amdgcn_ballot_w64(empty); m; m &= m - 1) zero(r0 + __builtin_ctzll(m), lane);
+    const int64_t r0 = (int64_t)blockIdx.x * kPadRows;
+    const bool empty = lane < kPadRows && r0 + lane < capacity && src[r0 + lane] < 0;
+    for (uint64_t m = __builtin_amdgcn_ballot_w64(empty); m; m &= m - 1) zero(r0 + __builtin_ctzll(m));
 }
-__device__ __forceinline__ void zero_bytes(uint8_t* p, int64_t n, int lane) {   // 16-byte aligned, whole 16 bytes
-    for (int64_t i = lane * 16; i < n; i += 64 * 16) store<false>(reinterpret_cast<v4u*>(p + i), v4u{});
+__device__ __forceinline__ void zero_bytes(uint8_t* p, int64_t n) {   // 16-byte aligned, whole 16 bytes
+    for (int64_t i = threadIdx.x * 16; i < n; i += blockDim.x * 16) store<false>(reinterpret_cast<v4u*>(p + i), v4u{});
 }
 
 struct GatherArgs {
@@ -269,11 +271,11 @@ __device__ __forceinline__ int64_t row_size(int64_t n) {
 template <int FORMAT>
 __global__ __launch_bounds__(kRouteThreads) void k_route_gather(GatherArgs A) {
     if (blockIdx.x < (uint32_t)A.pad_groups) {
-        zero_rows(A.src, A.capacity, [&](int64_t row, int lane) {
+        zero_rows(A.src, A.capacity, [&](int64_t row) {
             const int64_t size = row_size<FORMAT>(A.N);
-            zero_bytes(A.q + row * size, size, lane);
+            zero_bytes(A.q + row * size, size);
             if constexpr (FORMAT != ROW_BF16)
-                for (int i = lane; i < A.N / 32; i += 64) store_u8(A.e + row * (A.N / 32) + i, 0);
+                for (int i = threadIdx.x; i < A.N / 32; i += kRouteThreads) store_u8(A.e + row * (A.N / 32) + i, 0);
         });
         return;
     }
@@ -360,9 +362,7 @@ struct CombineGradArgs {
 template <int TH>
 __global__ __launch_bounds__(TH) void k_route_combine_grad(CombineGradArgs A) {
     if (blockIdx.x < (uint32_t)A.pad_groups) {
-        zero_rows(A.src, A.capacity, [&](int64_t row, int lane) {
-            zero_bytes(reinterpret_cast<uint8_t*>(A.dy + row * A.N), 2 * (int64_t)A.N, lane);
-        });
+        zero_rows(A.src, A.capacity, [&](int64_t row) { zero_bytes(reinterpret_cast<uint8_t*>(A.dy + row * A.N), 2 * (int64_t)A.N); });
         return;
     }
     __shared__ float part[TH / 64][8];

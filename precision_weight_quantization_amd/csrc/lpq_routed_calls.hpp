@@ -62,14 +62,12 @@ lpq_status route_shape(int64_t tokens, int64_t k, int64_t capacity, int64_t N) {
     return LPQ_OK;
 }
 
-int64_t pad_groups(int64_t capacity, int threads) { return ceil_div(capacity, threads); }   // a wave to 64 rows
-
 template <int FORMAT>
 lpq_status route_gather(const uint16_t* x, int64_t tokens, int64_t N, const int32_t* rows, int64_t k, const int32_t* src,
                         int64_t capacity, void* q, uint8_t* e, void* stream) {
     const lpq_status st = route_shape(tokens, k, capacity, N);
     if (st != LPQ_OK) return st;
-    const int64_t pad = pad_groups(capacity, kRouteThreads), blocks = pad + ceil_div(tokens * (N / 8), kRouteThreads);
+    const int64_t pad = ceil_div(capacity, kPadRows), blocks = pad + ceil_div(tokens * (N / 8), kRouteThreads);
     if (blocks > max_groups(kRouteThreads)) return LPQ_ERR_SHAPE;
     if (!x || !rows || !src || !q || (FORMAT != ROW_BF16 && !e)) return LPQ_ERR_NULL;
     if (!aligned(x, 16) || !aligned(q, 16) || !aligned(rows, 4) || !aligned(src, 4)) return LPQ_ERR_ALIGN;
@@ -518,7 +516,7 @@ lpq_status lpq_route_combine_backward(const uint16_t* dout, const uint16_t* y, i
     if (st != LPQ_OK) return st;
     const bool wide = N > 512;   // one wave to a row of up to 64 vectors
     const int threads = wide ? 256 : 64;
-    const int64_t pad = pad_groups(capacity, threads), blocks = pad + tokens;
+    const int64_t pad = ceil_div(capacity, kPadRows), blocks = pad + tokens;
     if (blocks > max_groups(threads)) return LPQ_ERR_SHAPE;
     if (!dout || !rows || !src || !dy || (dweights && !y)) return LPQ_ERR_NULL;
     if (!aligned(dout, 16) || !aligned(y, 16) || !aligned(dy, 16) || !aligned(rows, 4) || !aligned(src, 4) || !aligned(weights, 4) ||
