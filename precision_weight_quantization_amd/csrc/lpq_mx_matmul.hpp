@@ -550,6 +550,7 @@ __device__ __forceinline__ void mx_matmul_tiles(const MatmulArgs& A, int tiles_n
     sv = read_scales(0);
 
     int buf = 0;
+    bool stored = false;   // the last tile's results left in a known number of stores
     for (int tile = first_tile; tile < run_end; tile += slots) {
         clear();
         const int steps = steps_of(k);
@@ -579,7 +580,15 @@ __device__ __forceinline__ void mx_matmul_tiles(const MatmulArgs& A, int tiles_n
             pin();
             const int next_step = s + 1 == steps ? 0 : s + 1;
             if (next_step % kGroup == 0) put_scales(parity ^ 1);
-            lds_arrived();
+            // Behind a tile's stores the loads that are waited for are older than those (the stage after
+            // next was asked for before them): the stores, 16 bytes of each lane, may go on.
+            // A short contraction has few stages to hide them behind.
+            if (MODE == ROUTED_K && s == 0 && stored) {
+                if (A.f32) __asm__ volatile("s_waitcnt vmcnt(%0)" ::"n"(FM * FN) : "memory");
+                else __asm__ volatile("s_waitcnt vmcnt(%0)" ::"n"(FM * FN / 2) : "memory");
+            } else {
+                lds_arrived();
+            }
             const int step_k = MODE == ROUTED_K && next_step == 0 ? next_k : k;   // of the stage that comes
             if (next_step == full_of(step_k)) zero_tail(step_k, next_step, buf ^ 1);
             __syncthreads();
@@ -657,7 +666,8 @@ __device__ __forceinline__ void mx_matmul_tiles(const MatmulArgs& A, int tiles_n
                 }
             }
         };
-        if ((MODE != DENSE && TN == 256) || (A.f32 ? N % 4 == 0 : N % 8 == 0)) {
+        if (A.f32 ? N % 4 == 0 : N % 8 == 0) {
+            stored = true;
             if (whole_lines) {
                 if (A.f32) store_rows(std::true_type{}, std::true_type{});
                 else store_rows(std::false_type{}, std::true_type{});
@@ -666,7 +676,7 @@ __device__ __forceinline__ void mx_matmul_tiles(const MatmulArgs& A, int tiles_n
                 else store_rows(std::false_type{}, std::false_type{});
             }
         } else if constexpr (MODE != DENSE) {
-            // Rows that no vector divides (128 x 128 tiles only): by way of LDS too, then element by element along a row
+            // Rows that no vector divides: by way of LDS too, then element by element along a row
             // (from the accumulators, one element of 16 rows by 4 columns at a time: 30 us instead of 20 for
             // 4206 rows of 60 groups, 1021 x 1056, MXFP4 with an FP32 result).
             auto store_elements = [&](auto f32) {

@@ -141,9 +141,6 @@ struct RoutedLaunch {
     }
 };
 
-// Rows of y in vectors of 16 bytes, which the large tiles store.
-bool whole_vectors(const MatmulArgs& A) { return A.f32 ? A.N % 4 == 0 : A.N % 8 == 0; }
-
 // Which kernel, by the rows that a group has on average (the counts themselves are on the device).  Both
 // sides were timed with k = 2048 or 768, N = 1536 or 2048, 128 groups, MXFP8 unless said, rows drawn at random; us:
 //  * Tiles by way of LDS from 24 rows on: 19 rows 133 in tiles, 110 by rows; 25 rows 54 and 59 (k = 768);
@@ -161,7 +158,7 @@ lpq_status mx_matmul_routed(const MatmulArgs& A, const Routing& R, hipStream_t s
     const int64_t average = R.capacity / R.groups;
     const bool limits = A.K > 128 * stage_steps<FP4B, FP4A>() && A.K <= (1 << 22) && A.N <= (1 << 22);
     if (limits && average >= 24 && A.N >= 128 && R.capacity >= 128) {
-        if (average >= 144 && A.N >= 256 && whole_vectors(A) && R.capacity >= 256) return L.template tile<256, 256, 2, 4>();
+        if (average >= 144 && A.N >= 256 && R.capacity >= 256) return L.template tile<256, 256, 2, 4>();
         return L.template tile<128, 128, 2, 2>();
     }
     const int64_t steps = ceil_div(A.K, 128), tiles = L.row_tiles(16) * ceil_div(A.N, 64);
@@ -181,7 +178,7 @@ lpq_status mx_matmul_routed_dw(const MatmulArgs& A, const Routing& R, hipStream_
     const RoutedLaunch<FP4A, FP4B, ROUTED_K> L{A, R, s};
     const bool limits = A.K <= (1 << 22) && A.N <= (1 << 22);
     if (limits && A.M >= 128 && A.N >= 128) {
-        if (A.M >= 256 && A.N >= 256 && whole_vectors(A)) return L.template tile<256, 256, 2, 4>();
+        if (A.M >= 256 && A.N >= 256) return L.template tile<256, 256, 2, 4>();
         return L.template tile<128, 128, 2, 2>();
     }
     return L.template rows<2, 2, 1, 4>();
