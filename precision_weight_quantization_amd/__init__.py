@@ -1021,11 +1021,17 @@ _ROUTED = ("lpq_route_capacity", "lpq_route_plan", "lpq_route_gather", "lpq_rout
            "lpq_adapters", "lpq_adapters_backward", "lpq_mx_matmul_routed", "lpq_mx_matmul_routed_dw", "lpq_route_combine", "lpq_route_combine_backward")
 
 
+_found = {}
+
+
 def __getattr__(name):
-    if name in _ROUTED:
+    fn = _found.get(name)
+    if fn is None:
+        if name not in _ROUTED:
+            raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
         from . import routed
-        return getattr(routed, name)
-    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+        fn = _found[name] = getattr(routed, name)
+    return fn
 
 
 def __dir__():

@@ -141,25 +141,31 @@ struct RoutedLaunch {
     }
 };
 
-// Which kernel, by the rows that a group has on average (the counts themselves are on the device).  Both
-// sides were timed with k = 2048 or 768, N = 1536 or 2048, 128 groups, MXFP8 unless said, rows drawn at random; us:
-//  * Tiles by way of LDS from 24 rows on: 19 rows 133 in tiles, 110 by rows; 25 rows 54 and 59 (k = 768);
-//    37 rows 97 and 142; 56 rows 93 and 177.  A tile's stages take as long as its weights, whatever its rows.
-//  * 256 x 256 from 144 rows on: 75 rows 130 against 101 with 128 x 128, 125 rows 108 and 102 (MXFP4 weights), 150
-//    rows 123 and 149, 200 rows 134 and 157; 250 rows 186 and 178, where most groups just need a second tile.
+// Which kernel, by the rows that a group has on average (the counts themselves are on the device).  All sides
+// were timed with rows drawn for 128 groups of N = 1536, k = 2048 or N = 2048, k = 768 unless said, some experts liked
+// more than others; us, MXFP8 unless said:
+//  * Tiles by way of LDS from 6 rows on: 4 rows 69 in tiles of 64 rows and 73 by rows, but 27 and 25 with MXFP4
+//    weights (k = 768), 12 and 11 for 60 groups of 1024 x 1056; 6 rows 71 and 84; 8 rows 74 and 91. A tile's stages take
+//    as long as its weights, whatever its rows.
+//  * 128 x 64 tiles below 72 rows: 8 rows 74, with 128 x 128 81; 50 rows 108 and 107; 70 rows of 60 groups of 1024 x
+//    1056 20 and 24; 75 rows 120 and 112, evenly routed 139 and 101.
+//  * 256 x 256 from 144 rows on (evenly routed): 75 rows 130 against 101 with 128 x 128, 125 rows 108 and 102 (MXFP4
+//    weights), 150 rows 123 and 149, 200 rows 134 and 157; 250 rows 186 and 178, where most groups just need a second
+//    tile.  256 x 128: 163 at 150 rows, 323 instead of 276 for the workload of 512.
 //  * Rows: 16 rows a tile up to 16 on average, 32 above.  Columns of a wave: as many as leave a few waves for each
 //    SIMD (1 token of 8 experts, N = 2048, k = 768, MXFP4 weights: 4.7 with 16 columns, 5.6 with 32, 7.8 with 64; 24
-//    tokens 31, 27 and 25).
-//    Waves that share out k: of 3 steps at least (24 tokens, N = 2048, k = 768: 37 with 8, 31 with 2, 27 with 1;
-//    4 tokens, N = 4096, k = 7168: 167 with 8, 179 with 4).
+//    tokens 31, 27 and 25; where k is long the loads in flight count: 4 tokens, N = 4096, k = 7168 161 with 32, 186
+//    with 64).  Waves that share out k: of 3 steps at least (24 tokens, N = 2048, k = 768: 37 with 8, 31 with 2, 27 with
+//    1; 4 tokens, N = 4096, k = 7168: 167 with 8, 179 with 4).
 template <bool FP4A, bool FP4B>
 lpq_status mx_matmul_routed(const MatmulArgs& A, const Routing& R, hipStream_t s) {
     const RoutedLaunch<FP4A, FP4B, ROUTED_ROWS> L{A, R, s};
     const int64_t average = R.capacity / R.groups;
     const bool limits = A.K > 128 * stage_steps<FP4B, FP4A>() && A.K <= (1 << 22) && A.N <= (1 << 22);
-    if (limits && average >= 24 && A.N >= 128 && R.capacity >= 128) {
+    if (limits && average >= 6 && A.N >= 128 && R.capacity >= 64) {
         if (average >= 144 && A.N >= 256 && R.capacity >= 256) return L.template tile<256, 256, 2, 4>();
-        return L.template tile<128, 128, 2, 2>();
+        if (average >= 72 && R.capacity >= 128) return L.template tile<128, 128, 2, 2>();
+        return L.template tile<128, 64, 2, 2>();
     }
     const int64_t steps = ceil_div(A.K, 128), tiles = L.row_tiles(16) * ceil_div(A.N, 64);
     auto by_share = [&](auto nt, auto mt, auto u) {
@@ -168,7 +174,7 @@ lpq_status mx_matmul_routed(const MatmulArgs& A, const Routing& R, hipStream_t s
         if (steps >= 12) return L.template rows<NT, MT, U, 4>();
         return steps >= 6 ? L.template rows<NT, MT, U, 2>() : L.template rows<NT, MT, U, 1>();
     };
-    if (average > 16) return by_share(Int<4>{}, Int<2>{}, Int<1>{});   // 19 rows: 110, and 128 with 32 columns
+    if (average > 16) return by_share(Int<4>{}, Int<2>{}, Int<1>{});
     if (tiles > 2048 && steps < 24) return by_share(Int<4>{}, Int<1>{}, Int<1>{});
     return tiles > 512 ? by_share(Int<2>{}, Int<1>{}, Int<3>{}) : by_share(Int<1>{}, Int<1>{}, Int<3>{});
 }

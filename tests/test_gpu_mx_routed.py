@@ -42,7 +42,8 @@ def sizes_of(groups, most, seed, empty=0.3):
 ROWS = [([1], 0, 0, 1, 32), ([0, 3, 0], 0, 5, 40, 96), ([1, 0, 0, 5], 3, 2, 130, 160), ([16, 17, 0, 33, 1], 0, 0, 96, 1056),
         ([0, 0], 0, 40, 64, 128), (sizes_of(130, 3, 1), 1, 7, 144, 768), (sizes_of(64, 40, 2), 0, 100, 257, 544),
         (sizes_of(1024, 2, 3, 0.8), 0, 11, 72, 288), (sizes_of(37, 25, 4), 9, 0, 2053, 416),
-        # tiles: 128 x 128, then 256 x 256; whole, ragged, one row, none, one stage and many
+        # tiles: 128 x 64, 128 x 128, then 256 x 256; whole, ragged, one row, none, one stage and many
+        ([64, 0, 63, 65, 1, 30], 3, 0, 128, 544), (sizes_of(90, 30, 9), 0, 5, 390, 1056), ([6, 6, 60, 0, 8], 0, 0, 136, 512),
         ([128, 128, 128], 0, 0, 256, 512), ([100, 0, 1, 129, 200], 5, 3, 130, 288), ([1, 1, 380], 0, 40, 200, 1056),
         ([0, 0, 0, 0], 100, 300, 160, 416), (sizes_of(70, 300, 5), 3, 0, 264, 544), (sizes_of(130, 200, 6), 0, 60, 129, 320),
         ([256, 256], 0, 0, 512, 1024), ([257, 511, 0, 1, 300], 7, 11, 520, 288), ([700], 0, 0, 256, 544), ([10, 1300, 2], 0, 500, 1021, 1056),
