@@ -201,6 +201,10 @@ struct Stage {
 __device__ __forceinline__ void load_to_lds(const uint8_t* base, uint32_t offset, uint32_t to) {
     __asm__ volatile("s_nop 4\n\tglobal_load_lds_dwordx4 %1, %2" ::"{m0}"(to), "v"(offset), "s"(uniform_ptr(base)) : "memory");
 }
+// The same with 4 bytes of each lane from an address of its own, to byte `to` + 4 * l.
+__device__ __forceinline__ void load_word_to_lds(const uint8_t* p, uint32_t to) {
+    __asm__ volatile("s_nop 4\n\tglobal_load_lds_dword %1, off" ::"{m0}"(to), "v"(p) : "memory");
+}
 __device__ __forceinline__ void lds_arrived() { __asm__ volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 
 // The order of tiles.  Workgroups go to the 8 XCDs in turn, and each XCD has an
@@ -351,11 +355,44 @@ __device__ __forceinline__ void mx_matmul_tiles(const MatmulArgs& A, int tiles_n
 #pragma unroll
     for (int i = 0; i < SR; i++)
         off_s[i] = (uint32_t)(i * T / 64 + wave < kChunksB ? lane : min(lane, kRowsA - 1)) * blocks;
+    // ROUTED_K: the operands of the next group, one word of each 128 bytes, into L2.  A stage reads 128
+    // bytes of rows that lie a whole pitch apart, and memory gives those slowly (128 groups of 512 rows,
+    // 1536 x 2048, operands not in a cache: 286 us with these loads and 319 without; groups that begin inside
+    // a line 303 and 384; uneven groups 446 and 454).  Each workgroup of an XCD asks for its share, row by
+    // row, beside the stages of the present group.
+    int ahead_group = -1, ahead = 0, ahead_end = 0, ahead_lines_b = 1, ahead_lines_a = 1, ahead_k0 = 0, ahead_k = 0;
+    auto open_ahead = [&](int group) {   // called where a tile of `group` is opened
+        if (MODE != ROUTED_K || group + 1 <= ahead_group || (group + 1) * total >= run_end) return;
+        ahead_group = group + 1;
+        const RouteRun r = wave_run(routing, ahead_group);
+        ahead_k0 = r.first / 32 * 32;
+        ahead_k = r.last / 32 * 32 - ahead_k0;
+        ahead_lines_b = (row_bytes<FP4B>(ahead_k) + 127) / 128;
+        ahead_lines_a = (row_bytes<FP4A>(ahead_k) + 127) / 128;
+        const int64_t lines = (int64_t)A.N * ahead_lines_b + (int64_t)A.M * ahead_lines_a, slot = blockIdx.x / kXcds;
+        const int64_t counted = lines < (int64_t)1 << 30 ? lines : 0;   // indexes are 32-bit
+        ahead = (int)(counted * slot / slots);
+        ahead_end = (int)(counted * (slot + 1) / slots);
+    };
+    // one word for each thread; every lane loads, so that a wave's count of loads is known
+    auto load_ahead = [&]() {
+        const int i = min(ahead + tid, ahead_end - 1), lines_b = A.N * ahead_lines_b;
+        const bool of_b = i < lines_b;
+        const int j = of_b ? i : i - lines_b, lines = of_b ? ahead_lines_b : ahead_lines_a, row = j / lines;
+        const int bytes = of_b ? row_bytes<FP4B>(ahead_k) : row_bytes<FP4A>(ahead_k);
+        const uint8_t* p = (of_b ? A.b + row_bytes<FP4B>(ahead_k0) : A.a + row_bytes<FP4A>(ahead_k0)) +
+                           (int64_t)row * (of_b ? pitch_b : pitch_a) + min((j - row * lines) * 128, bytes - 4);
+        load_word_to_lds(p, lds0 + kOut + wave * 2048);   // where the wave's results go by later
+        ahead += T;
+    };
     auto open_tile = [&]() {
         const Tile t = tile_of(load_tile);
         int64_t n0 = t.n0, m0 = t.m0;
         if constexpr (MODE == ROUTED_ROWS) n0 += (int64_t)t.group * A.N;
-        if constexpr (MODE == ROUTED_K) load_k = t.k;
+        if constexpr (MODE == ROUTED_K) {
+            load_k = t.k;
+            if (steps_of(load_k) > 2) open_ahead(t.group);   // fewer stages leave no place for these loads
+        }
         gb = A.b + n0 * pitch_b + row_bytes<FP4B>(t.k0);
         ga = A.a + m0 * pitch_a + row_bytes<FP4A>(t.k0);
 #pragma unroll
@@ -429,12 +466,14 @@ __device__ __forceinline__ void mx_matmul_tiles(const MatmulArgs& A, int tiles_n
         for (int i = 0; i < LB; i++) load_to_lds(pb + (int64_t)i * (T / CB) * pitch_b, ob, to + i * T * 16);
 #pragma unroll
         for (int i = 0; i < LA; i++) load_to_lds(pa + (int64_t)i * (T / CA) * pitch_a, oa, to + TN * PB + i * T * 16);
-        if (load_step % kGroup == 0) load_scales(load_step / kGroup);
+        const bool with_scales = load_step % kGroup == 0;
+        if (with_scales) load_scales(load_step / kGroup);
         if (++load_step == steps_of(load_k)) {
             load_step = 0;
             load_tile += slots;
             if (load_tile < run_end) open_tile();
         }
+        return with_scales;
     };
     // the pieces of stage `step` that are past k, each lane its own
     auto zero_tail = [&](int k, int step, int buf) {
@@ -550,6 +589,7 @@ __device__ __forceinline__ void mx_matmul_tiles(const MatmulArgs& A, int tiles_n
     sv = read_scales(0);
 
     int buf = 0;
+    bool beside = false;   // the last stage's loads end with a load_ahead()
     bool stored = false;   // the last tile's results left in a known number of stores
     for (int tile = first_tile; tile < run_end; tile += slots) {
         clear();
@@ -586,13 +626,21 @@ __device__ __forceinline__ void mx_matmul_tiles(const MatmulArgs& A, int tiles_n
             if (MODE == ROUTED_K && s == 0 && stored) {
                 if (A.f32) __asm__ volatile("s_waitcnt vmcnt(%0)" ::"n"(FM * FN) : "memory");
                 else __asm__ volatile("s_waitcnt vmcnt(%0)" ::"n"(FM * FN / 2) : "memory");
+            } else if (MODE == ROUTED_K && beside && s + 1 < steps) {
+                __asm__ volatile("s_waitcnt vmcnt(1)" ::: "memory");   // all but the last stage's load_ahead()
             } else {
                 lds_arrived();
             }
             const int step_k = MODE == ROUTED_K && next_step == 0 ? next_k : k;   // of the stage that comes
             if (next_step == full_of(step_k)) zero_tail(step_k, next_step, buf ^ 1);
             __syncthreads();
-            if (load_tile < run_end) load_stage(buf);   // of this tile or of the next
+            bool scales_next = true;
+            if (load_tile < run_end) scales_next = load_stage(buf);   // of this tile or of the next
+            if constexpr (MODE == ROUTED_K) {
+                // not behind scales, whose wait would be for this too, nor before results go through the same LDS
+                beside = !scales_next && s + 1 < steps && ahead < ahead_end;
+                if (beside) load_ahead();
+            }
             buf ^= 1;
             parity ^= next_step % kGroup == 0;
             b0 ^= kNextCodes, b1 ^= kNextCodes, a0 ^= kNextCodes, a1 ^= kNextCodes;

@@ -81,7 +81,7 @@ def test_rows(lpq, case, fmts):
 SUMS = [([32], 0, 0, 1, 1), ([0, 64, 0], 32, 32, 40, 17), ([32, 0, 160, 1056], 0, 0, 100, 300), ([64] * 40 + [0] * 30, 0, 64, 33, 70),
         # tiles: of 128 x 128, then of 256 x 256; groups of no stage, a part of one, one, several
         ([128, 256, 512], 0, 0, 128, 128), ([0, 32, 64, 96, 0, 160], 32, 0, 130, 200), ([0, 0, 0], 64, 32, 256, 128),
-        ([32] * 300, 0, 0, 136, 129), ([2048, 0, 544, 2080], 0, 96, 255, 512), ([416, 128, 0, 384], 0, 0, 256, 256),
+        ([32] * 300, 0, 0, 136, 129), ([544, 32, 0, 1600, 64] * 12, 32, 0, 512, 776), ([320] * 70, 0, 64, 517, 512), ([2048, 0, 544, 2080], 0, 96, 255, 512), ([416, 128, 0, 384], 0, 0, 256, 256),
         ([0, 32, 0, 64, 96, 1056, 128, 0], 32, 64, 520, 264), ([32 * s for s in sizes_of(50, 20, 8)], 0, 0, 300, 513), ([0], 0, 32, 512, 256)]
 
 
