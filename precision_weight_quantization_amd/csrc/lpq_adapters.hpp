@@ -421,14 +421,14 @@ struct AdapterGradPair {
 
 // out[g][j][c] = s_g * sum over the rows of g of v[row][j] x[token][c]: a workgroup takes 128
 // columns, up to 64 elements of the rank and one part of the group's rows, which its waves share
-// out in steps of 32; their sums are added through LDS, in wave order.  A lane loads 8 x 8
+// out in steps of 32; their sums are added through LDS, in a fixed order.  A lane loads 8 x 8
 // pieces of x, 8 rows by 8 columns; column p of all pieces makes the second operand of one
 // instruction: its row l % 16 is column 8 * (l % 16) + p.
 constexpr int kGradWaves = 4;
 template <int JT>
-__global__ __launch_bounds__(64 * kGradWaves) void k_adapter_grad(AdapterGradPair P, Routing R) {
+__global__ __launch_bounds__(64 * kGradWaves, 2) void k_adapter_grad(AdapterGradPair P, Routing R) {
     constexpr int W = kGradWaves;
-    __shared__ v4f part[W][JT][8][64];
+    __shared__ v4f part[W / 2][JT][8][64];
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, g = lane >> 4, r = lane & 15;
     const bool second = (int)blockIdx.x >= P.a[0].blocks;
     const AdapterGradArgs& A = P.a[second];
@@ -473,22 +473,30 @@ __global__ __launch_bounds__(64 * kGradWaves) void k_adapter_grad(AdapterGradPai
                 for (int s = 2; s >= 0; s--) c[j][p] = mfma_bf16(v[j][s], xc, c[j][p]);
         }
     }
+    // two waves' sums to the other two, theirs to all four: half the LDS of all at once, so that two
+    // workgroups fit a CU with 64 elements of the rank
+    auto put = [&](int to) {
 #pragma unroll
-    for (int j = 0; j < JT; j++)
+        for (int j = 0; j < JT; j++)
 #pragma unroll
-        for (int p = 0; p < 8; p++) part[wave][j][p][lane] = c[j][p];
+            for (int p = 0; p < 8; p++) part[to][j][p][lane] = c[j][p];
+    };
+    if (wave >= W / 2) put(wave - W / 2);
+    __syncthreads();
+    if (wave < W / 2) {
+#pragma unroll
+        for (int j = 0; j < JT; j++)
+#pragma unroll
+            for (int p = 0; p < 8; p++) c[j][p] += part[wave][j][p][lane];
+        put(wave);
+    }
     __syncthreads();
     // a wave finishes every 4th tile of the rank: for each of its lane's 4 elements 8 neighbouring columns
     float* out = A.out + ((int64_t)split * R.groups + group) * P.rank * A.C;
     for (int j = wave; j < JT; j += W) {
         v4f s[8];
 #pragma unroll
-        for (int p = 0; p < 8; p++) {
-            s[p] = part[0][j][p][lane];
-#pragma unroll
-            for (int i = 1; i < W; i++) s[p] += part[i][j][p][lane];
-            s[p] *= scale;
-        }
+        for (int p = 0; p < 8; p++) s[p] = (part[0][j][p][lane] + part[1][j][p][lane]) * scale;
         const int at = j0 + j * 16 + 4 * g;   // 4 elements of the rank: rank % 8 == 0
         if (!in_c || at >= P.rank) continue;
         if (A.rank_last) {

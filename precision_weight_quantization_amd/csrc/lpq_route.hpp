@@ -235,7 +235,7 @@ __device__ __forceinline__ TokenVec token_vec(int64_t block, int64_t tokens, int
 }
 
 // Rows without a pair: a workgroup looks at kPadRows of them and calls zero(row) with all its
-// threads for each (a wave by itself for 64 rows: 62 us instead of 45 where 5,700 of 9,400
+// threads for each (a wave by itself for 64 rows: 62 us instead of 36 where 5,700 of 9,400
 // rows of 14 KB are empty, the last waves').
 constexpr int kPadRows = 16;
 template <typename F>

@@ -182,18 +182,22 @@ lpq_status mx_matmul_routed(const MatmulArgs& A, const Routing& R, hipStream_t s
 // Which tile, by rounds of the card as for the dense products: one of 256 x 256 counts 2, of 128 x 128 0.95
 // alone, 1.1 with two on each CU and 1.4 where many rounds keep memory busy.  us, 256 x 256 and 128 x 128: 128 groups
 // of 256 rows, 1536 x 2048 in MXFP8 271 and 376; of 32 rows 199 and 260; 96 groups of 32 rows, 520 x 776 in MXFP4 with an
-// FP32 result 60 and 54; 60 of 512 rows, 1024 x 1024 54 and 53; 8 of 4096 rows, 1024 x 1024 in MXFP8 58 and 42.
+// FP32 result 60 and 54; 60 of 512 rows, 1024 x 1024 54 and 53; 8 of 4096 rows, 1024 x 1024 in MXFP8 58 and 42.  Fewer than
+// 64 tiles of long contractions leave the card idle, and nothing shares out k: 32 x 32 by 8 waves then
+// (3 groups of 6269 rows, 288 x 344, MXFP4 and MXFP8: 23 us, in tiles 88).
 template <bool FP4A, bool FP4B>
 lpq_status mx_matmul_routed_dw(const MatmulArgs& A, const Routing& R, hipStream_t s) {
     const RoutedLaunch<FP4A, FP4B, ROUTED_K> L{A, R, s};
     const bool limits = A.K <= (1 << 22) && A.N <= (1 << 22);
-    if (limits && A.M >= 128 && A.N >= 128) {
-        const int64_t n128 = ceil_div(A.N, 128) * ceil_div(A.M, 128) * R.groups, n256 = ceil_div(A.N, 256) * ceil_div(A.M, 256) * R.groups;
+    const int64_t n128 = ceil_div(A.N, 128) * ceil_div(A.M, 128) * R.groups, steps = A.K / R.groups / 128;
+    if (limits && A.M >= 128 && A.N >= 128 && (n128 >= 64 || steps < 8)) {
+        const int64_t n256 = ceil_div(A.N, 256) * ceil_div(A.M, 256) * R.groups;
         const double c128 = n128 <= 256 ? 0.95 : ceil_div(n128, 512) * (n128 <= 2048 ? 1.1 : 1.4);
         if (A.M >= 256 && A.N >= 256 && 2.0 * ceil_div(n256, 256) < c128) return L.template tile<256, 256, 2, 4>();
         return L.template tile<128, 128, 2, 2>();
     }
-    return L.template rows<2, 2, 1, 4>();
+    if (steps >= 16) return L.template rows<2, 2, 2, 8>();
+    return steps >= 8 ? L.template rows<2, 2, 2, 4>() : L.template rows<2, 2, 2, 2>();
 }
 
 // Adapters of one shape: x [tokens, K], y [tokens, N], factors of `rank`, rows in a plan.
