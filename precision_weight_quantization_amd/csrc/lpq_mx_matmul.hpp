@@ -211,8 +211,8 @@ __device__ __forceinline__ void lds_arrived() { __asm__ volatile("s_waitcnt vmcn
 // L2 of its own: XCD x takes a run of tiles of its own, in columns of kTileGroup
 // rows of tiles, so that the workgroups that run on it at one time share few
 // rows of either operand.
-// Routed rows: 2, for a group has few tiles of rows that share its b (8: 3% slower with 512 rows a group
-// on average, 1536 x 2048).
+// Routed rows: 2, for a group has few tiles of rows that share its b (8: 290 us, 2: 282 with 512 rows a
+// group on average, 1536 x 2048).
 constexpr int kXcds = 8, kTileGroup = 8, kRoutedTileGroup = 2;
 template <int GROUP>
 __device__ __forceinline__ void tile_at(int t, int tiles_n, int tiles_m, int& n, int& m) {
@@ -288,7 +288,7 @@ __device__ __forceinline__ void mx_matmul_tiles(const MatmulArgs& A, int tiles_n
     int run = xcd * each + min(xcd, more), run_end = run + each + (xcd < more);
     if constexpr (MODE == ROUTED_K) {
         // The tiles of a group take as long as its contraction, so an XCD's run is its share of that
-        // rather than of the tiles (65536 rows of uneven groups, 1536 x 2048: 530 us by tiles).  In
+        // rather than of the tiles (65536 rows of 128 uneven groups, 1536 x 2048: 446 us, by tiles 523).  In
         // stages, where a tile's stores and start count as one, and as three at least.
         const RouteMap cost(routing, [&](const RouteRun& r) { return max(steps_of(r.last / 32 * 32 - r.first / 32 * 32), 3) + 1; });
         const int xcds = min(kXcds, (int)gridDim.x);
@@ -725,7 +725,7 @@ __device__ __forceinline__ void mx_matmul_tiles(const MatmulArgs& A, int tiles_n
             }
         } else if constexpr (MODE != DENSE) {
             // Rows that no vector divides: by way of LDS too, then element by element along a row
-            // (from the accumulators, one element of 16 rows by 4 columns at a time: 30 us instead of 20 for
+            // (from the accumulators, one element of 16 rows by 4 columns at a time: 27.7 us, not 24.5, for
             // 4206 rows of 60 groups, 1021 x 1056, MXFP4 with an FP32 result).
             auto store_elements = [&](auto f32) {
                 constexpr bool F32 = decltype(f32)::value;

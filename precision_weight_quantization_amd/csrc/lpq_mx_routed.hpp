@@ -12,7 +12,9 @@ namespace {
 // rows of its b.  ROUTED_K: y[g] = a[:, rows of g] b[:, rows of g]^T, 16 * MT rows of a, 16 * NT
 // of b.  W waves share out k in steps of 128 and add their results through LDS; a
 // workgroup holds 8 / W such tiles side by side, because a wave of few steps spends its time
-// on finding its group and on one round trip to memory.
+// on finding its group and on one round trip to memory.  Memory is the floor, the weights of the groups that
+// have rows: 24 tokens of 8 experts, N = 2048, k = 768, MXFP4 weights 15 us, 5.5 TB/s where the routing reaches 100 of 128
+// groups and four sets of weights take turns; N = 1536, k = 2048 in MXFP8 71 us, 4.4 TB/s from memory.
 template <bool FP4B, bool FP4A, int NT, int MT, int U, int W, TileMode MODE>
 __global__ __launch_bounds__(64 * kRowsWaves) void k_mx_matmul_routed_rows(MatmulArgs A, int tiles_n, int tiles_m, Routing routing,
                                                                            int first) {
