@@ -464,11 +464,22 @@ __global__ __launch_bounds__(64 * kGradWaves, 2) void k_adapter_grad(AdapterGrad
 #pragma unroll
         for (int j = 0; j < JT; j++)
 #pragma unroll
-            for (int s = 0; s < 3; s++) {   // rows of other groups meet zeros of x
+            for (int s = 0; s < 3; s++) {
                 v[j][s] = v4u{};
                 if (j0 + j * 16 + r < P.rank)   // a group begins at any row: 2-byte alignment
                     __builtin_memcpy(&v[j][s], A.planes + ((int64_t)s * P.rank + j0 + j * 16 + r) * P.pitch + row0 + 8 * g, 16);
             }
+        if (row0 + 32 > run.last) {   // the next group's rows: zeros of x alone would not keep its infinities and NaN out
+            const int kept = run.last - row0 - 8 * g;
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                const uint32_t mask = 2 * i + 1 < kept ? ~0u : 2 * i < kept ? 0xffffu : 0u;
+#pragma unroll
+                for (int j = 0; j < JT; j++)
+#pragma unroll
+                    for (int s = 0; s < 3; s++) v[j][s][i] &= mask;
+            }
+        }
 #pragma unroll
         for (int p = 0; p < 8; p++) {
             const v4u xc = piece_column(x, p);

@@ -140,6 +140,27 @@ def test_uneven(lpq, ids):
             assert bool((gA[g] == 0).all()) and bool((gB[g] == 0).all())
 
 
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("shape", [(100, 7, 16, 264, 520), (400, 5, 72, 136, 1032)])
+def test_not_finite(lpq, shape, value):
+    """What one adapter's tokens or factors hold shows in no other adapter's results."""
+    T, L = shape[:2]
+    ids = np.random.default_rng(9).integers(-1, L, T)
+    for where in ("x", "dy", "A", "B", "scale"):
+        c = Case(lpq, shape, spread=ids)
+        want, (wx, wA, wB) = c.forward(lpq), c.backward(lpq)
+        bad = torch.from_numpy(ids == 3).to(DEV)
+        t = getattr(c, where)
+        if where in ("x", "dy"):
+            t[bad] = value
+        else:
+            t[3] = value
+        got, (gx, gA, gB) = c.forward(lpq), c.backward(lpq)
+        others = [g for g in range(L) if g != 3]
+        assert same((got[~bad], gx[~bad], gA[others], gB[others]), (want[~bad], wx[~bad], wA[others], wB[others])), where
+        assert where == "dy" or not bool(got[bad].isfinite().any()), where
+
+
 def test_padded_plans(lpq):
     """A plan whose groups are padded, and one in a larger buffer, give the same results."""
     shape = (100, 7, 32, 264, 520)
