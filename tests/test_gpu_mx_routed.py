@@ -130,3 +130,52 @@ def test_offsets_outside_the_buffers(lpq, K, N, rows):
     for off in ([-5, 10, 1 << 30, -(1 << 31)], [32 * rows, 32 * rows + 9, 32 * rows - 3, 1 << 30], [(1 << 31) - 1, 0, 4, 1 << 30]):
         y = lpq.lpq_mx_matmul_routed_dw(at, ate, bt, bte, torch.tensor(off, dtype=torch.int32, device=DEV))
         assert y.shape == (3, N, N + 8)
+
+
+@pytest.mark.parametrize("groups,m,n", [(4, 40, 17), (5, 130, 200), (3, 256, 512)])
+def test_not_finite(lpq, groups, m, n):
+    """NaN codes and scale bytes of one group show in no other group's results."""
+    sizes = ([32, 96, 160, 64, 224] * 2)[:groups]
+    off = offsets_of(sizes, 0)
+    offsets = torch.tensor(off, dtype=torch.int32, device=DEV)
+    R, bad = off[-1], slice(off[1], off[2])
+    (a, ae, _), (b, be, _) = many(m, R, M.FP8, 3), many(n, R, M.FP8, 4)
+    others = [g for g in range(groups) if g != 1]
+    want = lpq.lpq_mx_matmul_routed_dw(a, ae, b, be, offsets)
+    a.view(torch.uint8)[:, bad] = 0x7f
+    be[:, bad.start // 32:bad.stop // 32] = 255
+    got = lpq.lpq_mx_matmul_routed_dw(a, ae, b, be, offsets)
+    assert torch.equal(got[others], want[others]) and bool(got[1].isnan().all())
+    (a, ae, _), (b, be, _) = many(R, 544, M.FP8, 5), many(groups * n, 544, M.FP4, 6)
+    b, be = b.view(groups, n, -1), be.view(groups, n, -1)
+    want = lpq.lpq_mx_matmul_routed(a, ae, b, be, offsets)
+    a.view(torch.uint8)[bad] = 0x7f
+    be[1] = 255
+    got = lpq.lpq_mx_matmul_routed(a, ae, b, be, offsets)
+    rows = torch.ones(R, dtype=torch.bool, device=DEV)
+    rows[bad] = False
+    assert torch.equal(got[rows], want[rows]) and bool(got[~rows].isnan().all())
+
+
+def test_past_32_bits(lpq):
+    """Results of more than 2^32 elements, or bytes behind 2^32 of them: the last group's rows, and its gradient."""
+    sizes = [270000, 0, 33]
+    off = offsets_of(sizes, 0)
+    offsets = torch.tensor(off, dtype=torch.int32, device=DEV)
+    R, N, K = off[-1], 16400, 288
+    a, ae, va = many(R, K, M.FP8, 1)
+    b, be, vb = many(3 * N, K, M.FP8, 2)
+    y = lpq.lpq_mx_matmul_routed(a, ae, b.view(3, N, K), be.view(3, N, -1), offsets)
+    assert y.numel() > 1 << 32
+    for r, g in ((slice(0, 40), 0), (slice(off[1] - 40, off[1]), 0), (slice(off[2], R), 2)):
+        w = vb[g * N:(g + 1) * N]
+        exact = va[r] @ w.T
+        assert bool(((y[r].double() - exact).abs() <= bound(va[r], w, exact, (M.FP8, M.FP8), False)).all())
+    del y, a, ae, va, b, be, vb
+    (a, ae, va), (b, be, vb) = many(8200, 65 * 32, M.FP8, 3), many(8208, 65 * 32, M.FP8, 4)
+    dw = lpq.lpq_mx_matmul_routed_dw(a, ae, b, be, torch.arange(66, dtype=torch.int32, device=DEV) * 32)
+    assert dw.numel() > 1 << 32
+    for g in (0, 64):
+        p, q = va[:, g * 32:g * 32 + 32], vb[:, g * 32:g * 32 + 32]
+        exact = p @ q.T
+        assert bool(((dw[g].double() - exact).abs() <= bound(p, q, exact, (M.FP8, M.FP8), False)).all())

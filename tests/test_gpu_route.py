@@ -141,3 +141,31 @@ def test_combine_backward(lpq, T, k, groups, N, align):
         assert none is None and torch.equal(only.view(torch.int16), gy.view(torch.int16))
         again = lpq.lpq_route_combine_backward(dout, rows, src, weights, y=y)
         assert torch.equal(again[1], gw)
+
+
+def test_past_32_bits(lpq):
+    """A routed matrix of more than 2^32 elements."""
+    T, k, N = 135000, 2, 16000
+    x = torch.randn((T, N), device=DEV, dtype=torch.bfloat16)
+    ids = torch.arange(2 * T, device=DEV, dtype=torch.int32).view(T, k) % 3
+    offsets, rows, src = lpq.lpq_route_plan(ids, 3, 32)
+    y = lpq.lpq_route_gather(x, rows, src)
+    assert y.numel() > 1 << 32
+    ends = torch.cat([torch.arange(300), torch.arange(T - 300, T)]).to(DEV)
+    for j in range(k):
+        assert torch.equal(y[rows[ends, j].long()], x[ends])
+    q, e = lpq.lpq_route_gather_mxfp8(x, rows, src)
+    want, scale = lpq.lpq_quantize_mxfp8(x[ends].contiguous())
+    u8 = lambda t: t.view(torch.uint8)
+    for j in range(k):
+        r = rows[ends, j].long()
+        assert torch.equal(u8(q)[r], u8(want)) and torch.equal(e[r], scale)
+    del q, e
+    out = lpq.lpq_route_combine(y, rows)   # exact: x + x
+    assert torch.equal(out[ends], 2 * x[ends])
+    del out
+    dy, dw = lpq.lpq_route_combine_backward(x, rows, src, None, y)
+    for j in range(k):
+        assert torch.equal(dy[rows[ends, j].long()], x[ends])
+    exact = x[ends].double().square().sum(1)   # N products of one sign, N + 12 roundings
+    assert bool(((dw[ends].double() - exact[:, None]).abs() <= (N + 12) * 2.0 ** -24 * exact[:, None]).all())
