@@ -4,7 +4,9 @@
  * their dequantizers and fake-quants (quantize-dequantize, "QDQ"); and the
  * microscaled linear layer: two-way quantization, the root-mean-square norm
  * with MXFP8 output and its gradients, and products of MXFP8 and MXFP4
- * matrices.
+ * matrices; and layers whose rows go to different weights: the plan that
+ * orders tokens by expert or adapter, gather, grouped products and their
+ * weight gradients, weighted combination, low-rank adapters.
  *
  * What the calls compute (web pages, cited by title and section):
  *  - "Low Precision RL" (Miles documentation), "Choose a precision" table and

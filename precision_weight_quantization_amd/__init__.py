@@ -12,7 +12,10 @@ Every call launches on the device of its tensors or of its table, whichever is
 current.  With a ``stream`` argument the MXFP4 calls and the microscaled linear
 layer (``lpq_quantize_mxfp8_transposed``, ``lpq_rmsnorm_mxfp8``,
 ``lpq_rmsnorm_backward``, ``lpq_mx_matmul`` and their like) allocate what they
-are not given on that stream, the others on the current one.
+are not given on that stream, the others on the current one.  The routed layers'
+calls (``lpq_route_plan``, ``lpq_route_gather``, ``lpq_route_combine``,
+``lpq_mx_matmul_routed``, ``lpq_adapters`` and their like) stand in the module
+``routed``, which the first use of one of their names here loads.
 
 If the library has not been built the import fails: there is no fallback.
 """

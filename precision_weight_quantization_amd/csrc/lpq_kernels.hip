@@ -8,7 +8,9 @@
 // plus the NVFP4 fake-quant; MXFP4 (E2M1, UE8M0 byte per 1x32 block).  The
 // codecs are streaming work bound by HBM bandwidth, and so are the two-way
 // quantizer and the root-mean-square norm of the quantized layer; its products
-// run on the matrix cores (lpq_mx_matmul.hpp).
+// run on the matrix cores (lpq_mx_matmul.hpp).  Layers whose rows go to
+// different weights: lpq_route.hpp, lpq_mx_routed.hpp, lpq_adapters.hpp and
+// their calls in lpq_routed_calls.hpp.
 //
 // Launch shape.  A grouped call covers many tensors in one launch.  The grid
 // is one-dimensional and dense: the host lays the tensors' work units
