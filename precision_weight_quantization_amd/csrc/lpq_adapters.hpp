@@ -17,7 +17,7 @@ namespace {
 // Measured (us; floors at a copy's 5.2 TB/s): 8192 tokens of 8 adapters, 9728 x 2560, rank 64: shrink 24
 // (8: its time is 8 for finding rows and the sums in LDS, 7 for x and 9 for A out of the caches), expand 86 (62).  40
 // tokens of 32 adapters, 4096 x 2560, rank 16: 4.0 and 4.6, latency.  Gradients, 4099 tokens of 4, 1024 x 2560, rank
-// 24: transpose 4.8, shrinks 12.5, planes 4.8, gradients 19 and their sum 6.4, expand 14, together 60 (14): six
+// 24: transpose 4.8, shrinks 12.5, planes 4.8, gradients 20 and their sum 6.4, expand 14, together 60 (14): six
 // launches, each of a few round trips to memory.
 // U is FP32.  It meets the BF16 matrix instruction as a sum of BF16 numbers: two for a BF16
 // result (off by 2^-17 of each term, its rounding is 2^-9), three, which is all 24 bits, for
