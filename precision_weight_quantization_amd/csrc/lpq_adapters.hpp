@@ -19,9 +19,8 @@ namespace {
 // tokens of 32 adapters, 4096 x 2560, rank 16: 4.0 and 4.6, latency.  Gradients, 4099 tokens of 4, 1024 x 2560, rank
 // 24: transpose 4.8, shrinks 12.5, planes 4.8, gradients 20 and their sum 6.4, expand 14, together 60 (14): six
 // launches, each of a few round trips to memory.
-// U is FP32.  It meets the BF16 matrix instruction as a sum of BF16 numbers: two for a BF16
-// result (off by 2^-17 of each term, its rounding is 2^-9), three, which is all 24 bits, for
-// the FP32 gradients.  Products of BF16 numbers are exact in FP32, so every sum is an FP32 one.
+// U is FP32.  It meets the BF16 matrix instruction as the sum of three BF16 numbers, which is all 24
+// bits.  Products of BF16 numbers are exact in FP32, so every sum is an FP32 one.
 // Memory is the floor: x, base and y once, and the adapters' factors.
 typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
 
@@ -148,12 +147,12 @@ struct ExpandArgs {
     int32_t copy_tiles;       // of 64 tokens: the first ones look for tokens without a row
 };
 
-// s_g u of a lane's row, 8 elements of the rank a step, as two BF16 numbers each.
+// s_g u of a lane's row, 8 elements of the rank a step, as three BF16 numbers each.
 template <int STEPS>
 struct ExpandRow {
     int64_t at;        // the row's first element in `in` and `out`
     bool in;           // there is a token
-    v4u hi[STEPS], lo[STEPS];
+    v4u hi[STEPS], mid[STEPS], lo[STEPS];
 };
 template <int STEPS>
 __device__ __forceinline__ ExpandRow<STEPS> expand_row(const ExpandArgs& A, const Routing& R, int group, int row, int last, int g) {
@@ -177,6 +176,7 @@ __device__ __forceinline__ ExpandRow<STEPS> expand_row(const ExpandArgs& A, cons
 #pragma unroll
         for (int i = 0; i < 4; i++) f[i] = a[i] * scale, f[4 + i] = b[i] * scale;
         e.hi[s] = take_bf16(f);
+        e.mid[s] = take_bf16(f);
         e.lo[s] = take_bf16(f);
     }
     return e;
@@ -209,6 +209,7 @@ __device__ __forceinline__ void expand_64(const ExpandArgs& A, const ExpandRow<S
         for (int s = 0; s < STEPS; s++) {
             const v4u w = weight(p, s);
             c[p] = mfma_bf16(w, e.lo[s], c[p]);
+            c[p] = mfma_bf16(w, e.mid[s], c[p]);
             c[p] = mfma_bf16(w, e.hi[s], c[p]);
         }
     }
