@@ -447,7 +447,10 @@ __global__ __launch_bounds__(64 * kGradWaves, 2) void k_adapter_grad(AdapterGrad
     const RouteRun run = wave_run(R, group);
     const int j0 = piece * 64, col = tile * 128 + 8 * r;
     const bool in_c = col < A.C;   // C % 8 == 0
-    const float scale = P.scale ? P.scale[group] : 1.0f;
+    // A part without a token adds nothing, whatever the scale: a group's tokens are its first rows.
+    const int earliest = run.first + split * W * 32;
+    const bool any = earliest < run.last && token_of(P.src, earliest, P.tokens) >= 0;
+    const float scale = !any ? 0.0f : P.scale ? P.scale[group] : 1.0f;
     v4f c[JT][8];
 #pragma unroll
     for (int j = 0; j < JT; j++)

@@ -8,6 +8,7 @@ import pytest
 import torch
 
 from tests.gpu_util import DEV
+from tests.test_gpu_rmsnorm import bf16
 
 pytestmark = pytest.mark.gpu
 
@@ -62,3 +63,38 @@ def test_all_bits_of_u(lpq, tokens, rank):
     dx, _, _ = lpq.lpq_adapters_backward(bf(x), bf(np.zeros((tokens, wide))), bf(second.transpose(0, 2, 1)), bf(first.transpose(0, 2, 1)),
                                          *plan, scale=s)
     assert torch.equal(dx.cpu(), want)
+
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("shape,align", [((40, 6, 16, 72, 136), 1), ((300, 40, 24, 640, 1032), 1), ((600, 3, 72, 264, 520), 32)])
+def test_scale_of_an_adapter_without_tokens(lpq, shape, align, value):
+    """It is in nobody's gradients: zeros for its own, or what was there.  Gradients of one part of the rows
+    and of several."""
+    T, L, r, N, K = shape
+    ids = np.arange(T) % (L - 1) + 1   # none goes to the first
+    plan = plan_of(lpq, ids, L, align)
+    rng = np.random.default_rng(T)
+    x, A, B, dy = (bf16(s, i).to(DEV) for i, s in enumerate(((T, K), (L, r, K), (L, N, r), (T, N))))
+    scale = torch.from_numpy(rng.uniform(0.5, 2, L).astype(np.float32)).to(DEV)
+    held = [torch.randn((L, r, K), device=DEV), torch.randn((L, N, r), device=DEV)]
+    call = lambda **k: lpq.lpq_adapters_backward(dy, x, A, B, *plan, scale=scale, **k)
+    plain, added = call(), call(dA=held[0].clone(), dB=held[1].clone(), accumulate=True)
+    scale[0] = value
+    for want, got in ((plain, call()), (added, call(dA=held[0].clone(), dB=held[1].clone(), accumulate=True))):
+        assert all(torch.equal(a, b) for a, b in zip(want, got))
+    assert bool((plain[1][0] == 0).all()) and bool((plain[2][0] == 0).all())
+    assert torch.equal(added[1][0], held[0][0]) and torch.equal(added[2][0], held[1][0])
+
+
+def test_infinite_scale_and_parts_without_tokens(lpq):
+    """A group's infinite gradients stay so where parts of its rows are empty, or padding: positive numbers, so that
+    every gradient is an infinity."""
+    T, L, r, N, K = 500, 4, 24, 136, 264
+    ids = np.where(np.arange(T) < 420, 3, np.arange(T) % 3)
+    x, A, B, dy = (bf16(s, i).abs().clamp(min=2.0 ** -6).to(DEV) for i, s in enumerate(((T, K), (L, r, K), (L, N, r), (T, N))))
+    scale = torch.ones(L, device=DEV)
+    scale[1] = float("inf")
+    for align in (1, 32, 1024):
+        _, dA, dB = lpq.lpq_adapters_backward(dy, x, A, B, *plan_of(lpq, ids, L, align), scale=scale)
+        for d in (dA, dB):
+            assert bool((d[1] == float("inf")).all()) and bool(d[[0, 2, 3]].isfinite().all())
