@@ -20,7 +20,8 @@ namespace {
 // 24: transpose 4.8, shrinks 12.5, planes 4.8, gradients 20 and their sum 6.4, expand 14, together 60 (14): six
 // launches, each of a few round trips to memory.
 // U is FP32.  It meets the BF16 matrix instruction as the sum of three BF16 numbers, which is all 24
-// bits.  Products of BF16 numbers are exact in FP32, so every sum is an FP32 one.
+// bits.  Products of BF16 numbers are exact in FP32, so every sum is an FP32 one.  An infinity meets the
+// first of the three alone: the others may be zeros or of the other sign, which would make a NaN of it.
 // Memory is the floor: x, base and y once, and the adapters' factors.
 typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
 
@@ -31,16 +32,47 @@ __device__ __forceinline__ v4f mfma_bf16(v4u a, v4u b, v4f c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, a), __builtin_bit_cast(v8bf, b), c, 0, 0, 0);
 }
 
-// 8 FP32 numbers as the BF16 vector nearest to them; they keep what is left.
+// The first 8 bits of each of 8 FP32 numbers as a BF16 vector; they keep what is left, which takes two more
+// of these.  FIRST: nothing is left of an infinity or a NaN (infinity - infinity would be a NaN).  Cut and not
+// rounded, so that no finite number becomes an infinity.
+template <bool FIRST, int N>
+__device__ __forceinline__ void take_bf16(float (&f)[N], uint32_t (&w)[N / 2]) {
+#pragma unroll
+    for (int i = 0; i < N; i += 2) {
+        w[i / 2] = __builtin_amdgcn_perm(__float_as_uint(f[i + 1]), __float_as_uint(f[i]), 0x07060302u);
+        f[i] -= bf16_lo(w[i / 2]);
+        f[i + 1] -= bf16_hi(w[i / 2]);
+        if constexpr (FIRST) {
+            f[i] = __builtin_isfinite(f[i]) ? f[i] : 0.0f;
+            f[i + 1] = __builtin_isfinite(f[i + 1]) ? f[i + 1] : 0.0f;
+        }
+    }
+}
+template <bool FIRST>
 __device__ __forceinline__ v4u take_bf16(float (&f)[8]) {
-    v4u w;
+    uint32_t w[4];
+    take_bf16<FIRST>(f, w);
+    return v4u{w[0], w[1], w[2], w[3]};
+}
+// Infinities and NaN among 8 BF16 numbers as zeros.
+__device__ __forceinline__ v4u finite_bf16(v4u v) {
 #pragma unroll
     for (int i = 0; i < 4; i++) {
-        w[i] = bf16x2(f[2 * i], f[2 * i + 1]);
-        f[2 * i] -= bf16_lo(w[i]);
-        f[2 * i + 1] -= bf16_hi(w[i]);
+        const uint32_t lo = (v[i] & 0x7f80u) == 0x7f80u ? 0u : 0xffffu, hi = (v[i] & 0x7f800000u) == 0x7f800000u ? 0u : 0xffff0000u;
+        v[i] &= lo | hi;
     }
-    return w;
+    return v;
+}
+
+// An infinity or a NaN among them.
+template <int N>
+__device__ __forceinline__ bool not_finite(const v4f (&c)[N]) {
+    float bad = 0.0f;
+#pragma unroll
+    for (int i = 0; i < N; i++)
+#pragma unroll
+        for (int j = 0; j < 4; j++) bad = __builtin_fmaf(c[i][j], 0.0f, bad);
+    return bad != bad;
 }
 
 // The token of a row; -1 where a plan that was not made for these tokens holds something else.
@@ -175,9 +207,9 @@ __device__ __forceinline__ ExpandRow<STEPS> expand_row(const ExpandArgs& A, cons
         }
 #pragma unroll
         for (int i = 0; i < 4; i++) f[i] = a[i] * scale, f[4 + i] = b[i] * scale;
-        e.hi[s] = take_bf16(f);
-        e.mid[s] = take_bf16(f);
-        e.lo[s] = take_bf16(f);
+        e.hi[s] = take_bf16<true>(f);
+        e.mid[s] = take_bf16<false>(f);
+        e.lo[s] = take_bf16<false>(f);
     }
     return e;
 }
@@ -201,28 +233,33 @@ __device__ __forceinline__ Base expand_base(const ExpandArgs& A, const ExpandRow
 template <int STEPS, typename F>
 __device__ __forceinline__ void expand_64(const ExpandArgs& A, const ExpandRow<STEPS>& e, const Base& base, int n0, int n_last, int g,
                                           F&& weight) {
-    v4f c[4];
-#pragma unroll
-    for (int p = 0; p < 4; p++) {
-        c[p] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-        for (int s = 0; s < STEPS; s++) {
-            const v4u w = weight(p, s);
-            c[p] = mfma_bf16(w, e.lo[s], c[p]);
-            c[p] = mfma_bf16(w, e.mid[s], c[p]);
-            c[p] = mfma_bf16(w, e.hi[s], c[p]);
-        }
-    }
 #pragma unroll
     for (int h = 0; h < 2; h++) {
+        v4f first[2], rest[2];   // sums with the first number, with the others
+#pragma unroll
+        for (int q = 0; q < 2; q++) {
+            first[q] = rest[q] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int s = 0; s < STEPS; s++) {
+                const v4u w = weight(2 * h + q, s);
+                rest[q] = mfma_bf16(w, e.lo[s], rest[q]);
+                rest[q] = mfma_bf16(w, e.mid[s], rest[q]);
+                first[q] = mfma_bf16(w, e.hi[s], first[q]);
+            }
+        }
         const int n = n0 + 32 * h + 8 * g;
         if (!e.in || n >= n_last) continue;
         const F8 f = widen8(base.h[h]);
         v4u o;
 #pragma unroll
         for (int i = 0; i < 4; i++) {
-            const v4f& d = c[2 * h + i / 2];
-            o[i] = bf16x2(f.x[2 * i] + d[(i & 1) * 2], f.x[2 * i + 1] + d[(i & 1) * 2 + 1]);
+            float d[2];
+#pragma unroll
+            for (int x = 0; x < 2; x++) {
+                const float a = first[i / 2][(i & 1) * 2 + x], b = rest[i / 2][(i & 1) * 2 + x];
+                d[x] = f.x[2 * i + x] + (__builtin_isfinite(a) ? a + b : a);
+            }
+            o[i] = bf16x2(d[0], d[1]);
         }
         store<false>(reinterpret_cast<v4u*>(A.out + e.at + n), o);
     }
@@ -401,9 +438,10 @@ __global__ __launch_bounds__(256) void k_adapter_planes(AdapterPlanesArgs A, Rou
     for (int i = 0; i < 4; i++) f[i] = tile[j][x + i];
 #pragma unroll
     for (int s = 0; s < 3; s++) {
-        const v2u w{bf16x2(f[0], f[1]), bf16x2(f[2], f[3])};
-        f[0] -= bf16_lo(w.x), f[1] -= bf16_hi(w.x), f[2] -= bf16_lo(w.y), f[3] -= bf16_hi(w.y);
-        store<false>(reinterpret_cast<v2u*>(A.planes[which] + ((int64_t)s * A.rank + j0 + j) * A.pitch + r0 + x), w);
+        uint32_t w[2];
+        if (s == 0) take_bf16<true>(f, w);
+        else take_bf16<false>(f, w);
+        store<false>(reinterpret_cast<v2u*>(A.planes[which] + ((int64_t)s * A.rank + j0 + j) * A.pitch + r0 + x), v2u{w[0], w[1]});
     }
 }
 
@@ -452,47 +490,55 @@ __global__ __launch_bounds__(64 * kGradWaves, 2) void k_adapter_grad(AdapterGrad
     const bool any = earliest < run.last && token_of(P.src, earliest, P.tokens) >= 0;
     const float scale = !any ? 0.0f : P.scale ? P.scale[group] : 1.0f;
     v4f c[JT][8];
-#pragma unroll
-    for (int j = 0; j < JT; j++)
-#pragma unroll
-        for (int p = 0; p < 8; p++) c[j][p] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-    for (int row0 = run.first + (split * W + wave) * 32; row0 < run.last; row0 += A.splits * W * 32) {
-        v4u x[8];
-#pragma unroll
-        for (int i = 0; i < 8; i++) {
-            const int row = row0 + 8 * g + i;
-            const int64_t t = row < run.last ? token_of(P.src, row, P.tokens) : -1;
-            x[i] = t >= 0 && in_c ? load<false>(reinterpret_cast<const v4u*>(A.x + t * A.C + col)) : v4u{};
-        }
-        v4u v[JT][3];
+    auto sums = [&](auto rest_finite) {
+        constexpr bool REST_FINITE = decltype(rest_finite)::value;   // infinities and NaN of x meet the first plane alone
 #pragma unroll
         for (int j = 0; j < JT; j++)
 #pragma unroll
-            for (int s = 0; s < 3; s++) {
-                v[j][s] = v4u{};
-                if (j0 + j * 16 + r < P.rank)   // a group begins at any row: 2-byte alignment
-                    __builtin_memcpy(&v[j][s], A.planes + ((int64_t)s * P.rank + j0 + j * 16 + r) * P.pitch + row0 + 8 * g, 16);
+            for (int p = 0; p < 8; p++) c[j][p] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+        for (int row0 = run.first + (split * W + wave) * 32; row0 < run.last; row0 += A.splits * W * 32) {
+            v4u x[8];
+#pragma unroll
+            for (int i = 0; i < 8; i++) {
+                const int row = row0 + 8 * g + i;
+                const int64_t t = row < run.last ? token_of(P.src, row, P.tokens) : -1;
+                x[i] = t >= 0 && in_c ? load<false>(reinterpret_cast<const v4u*>(A.x + t * A.C + col)) : v4u{};
             }
-        if (row0 + 32 > run.last) {   // the next group's rows: zeros of x alone would not keep its infinities and NaN out
-            const int kept = run.last - row0 - 8 * g;
-#pragma unroll
-            for (int i = 0; i < 4; i++) {
-                const uint32_t mask = 2 * i + 1 < kept ? ~0u : 2 * i < kept ? 0xffffu : 0u;
-#pragma unroll
-                for (int j = 0; j < JT; j++)
-#pragma unroll
-                    for (int s = 0; s < 3; s++) v[j][s][i] &= mask;
-            }
-        }
-#pragma unroll
-        for (int p = 0; p < 8; p++) {
-            const v4u xc = piece_column(x, p);
+            v4u v[JT][3];
 #pragma unroll
             for (int j = 0; j < JT; j++)
 #pragma unroll
-                for (int s = 2; s >= 0; s--) c[j][p] = mfma_bf16(v[j][s], xc, c[j][p]);
+                for (int s = 0; s < 3; s++) {
+                    v[j][s] = v4u{};
+                    if (j0 + j * 16 + r < P.rank)   // a group begins at any row: 2-byte alignment
+                        __builtin_memcpy(&v[j][s], A.planes + ((int64_t)s * P.rank + j0 + j * 16 + r) * P.pitch + row0 + 8 * g, 16);
+                }
+            if (row0 + 32 > run.last) {   // the next group's rows: zeros of x alone would not keep its infinities and NaN out
+                const int kept = run.last - row0 - 8 * g;
+#pragma unroll
+                for (int i = 0; i < 4; i++) {
+                    const uint32_t mask = 2 * i + 1 < kept ? ~0u : 2 * i < kept ? 0xffffu : 0u;
+#pragma unroll
+                    for (int j = 0; j < JT; j++)
+#pragma unroll
+                        for (int s = 0; s < 3; s++) v[j][s][i] &= mask;
+                }
+            }
+#pragma unroll
+            for (int p = 0; p < 8; p++) {
+                const v4u xc = piece_column(x, p), xf = REST_FINITE ? finite_bf16(xc) : xc;
+#pragma unroll
+                for (int j = 0; j < JT; j++)
+#pragma unroll
+                    for (int s = 2; s >= 0; s--) c[j][p] = mfma_bf16(v[j][s], s ? xf : xc, c[j][p]);
+            }
         }
-    }
+    };
+    sums(std::false_type{});
+    bool bad = false;
+#pragma unroll
+    for (int j = 0; j < JT; j++) bad |= not_finite(c[j]);
+    if (any_lane(bad)) sums(std::true_type{});   // the whole wave, once more
     // two waves' sums to the other two, theirs to all four: half the LDS of all at once, so that two
     // workgroups fit a CU with 64 elements of the rank
     auto put = [&](int to) {

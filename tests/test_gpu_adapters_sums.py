@@ -2,13 +2,17 @@
 and NaN make of them.
 
 Where a test asks for equality every sum in between is exact in FP32, so that the result is the 64-bit one
-rounded once; the others take test_gpu_adapters' tolerances."""
+rounded once.  The others take test_gpu_adapters' tolerances, with u in three BF16 numbers, which leave 2^-24 of
+it and not 2^-16; the second and third number's products are 2^-8 and 2^-16 of the first's, and so are the roundings of
+their sums: 1.01 times the first's."""
 import numpy as np
 import pytest
 import torch
 
+from tests import routed_ref as R
 from tests.gpu_util import DEV
-from tests.test_gpu_rmsnorm import bf16
+from tests.test_gpu_adapters import rounded
+from tests.test_gpu_rmsnorm import bf16, f64
 
 pytestmark = pytest.mark.gpu
 
@@ -98,3 +102,119 @@ def test_infinite_scale_and_parts_without_tokens(lpq):
         _, dA, dB = lpq.lpq_adapters_backward(dy, x, A, B, *plan_of(lpq, ids, L, align), scale=scale)
         for d in (dA, dB):
             assert bool((d[1] == float("inf")).all()) and bool(d[[0, 2, 3]].isfinite().all())
+
+
+# tokens, groups, rank, N, K: rows by waves of their own, tiles of 64, parts of the gradients' rows
+SHAPES = [(100, 7, 16, 264, 520), (400, 5, 72, 136, 1032), (900, 2, 24, 72, 264), (70, 1, 40, 2000, 64)]
+
+
+def kinds(t):
+    """0 finite, 1 and -1 infinite, 2 NaN."""
+    a = f64(t) if isinstance(t, torch.Tensor) else t
+    return np.where(np.isnan(a), 2, np.where(np.isinf(a), np.sign(a), 0)).astype(int)
+
+
+def positive(shape, seed, scale=1.0):
+    return bf16(shape, seed).abs().clamp(min=2.0 ** -6).mul(scale).to(torch.bfloat16).to(DEV)
+
+
+def check(lpq, c, ids, plan):
+    """Results and gradients against the formula: the same infinities, the same NaN, and near it elsewhere."""
+    L, r, K = c["A"].shape
+    N = c["B"].shape[1]
+    names = "dy x A B scale base dres".split()
+    d = {k: f64(c[k]) for k in names}
+    kept = np.where((ids >= 0) & (ids < L), ids, -1)
+    most = max(int((kept == g).sum()) for g in range(L))
+    with np.errstate(all="ignore"):
+        y, size = R.adapters(d["x"], d["A"], d["B"], ids, d["scale"], d["base"])
+        want = R.adapters_grad(d["dy"], d["x"], d["A"], d["B"], ids, d["scale"], d["dres"])
+        (dx, dA, dB), (sx, sA, sB) = want
+        tols = [rounded(y, 1.01 * (K + r + 19) * 2.0 ** -24 * size, size), rounded(dx, 1.01 * (N + r + 19) * 2.0 ** -24 * sx, sx),
+                1.01 * (N + most + 51) * 2.0 ** -24 * sA, 1.01 * (K + most + 51) * 2.0 ** -24 * sB]
+        got = [lpq.lpq_adapters(c["x"], c["A"], c["B"], *plan, scale=c["scale"], base=c["base"]),
+               *lpq.lpq_adapters_backward(c["dy"], c["x"], c["A"], c["B"], *plan, scale=c["scale"], dres=c["dres"])]
+        for name, g, w, tol in zip(("y", "dx", "dA", "dB"), got, (y, dx, dA, dB), tols):
+            assert np.array_equal(kinds(g), kinds(w)), (name, np.argwhere(kinds(g) != kinds(w))[:4])
+            at = np.isfinite(w)
+            assert (np.abs(f64(g) - w)[at] <= tol[at]).all(), name
+    return got, (y, dx, dA, dB)
+
+
+@pytest.mark.parametrize("value", [float("inf"), -float("inf"), float("nan")])
+@pytest.mark.parametrize("where", ["x", "dy", "A", "B"])
+@pytest.mark.parametrize("shape", SHAPES)
+def test_infinities_as_the_formula(lpq, shape, where, value):
+    """Factors and tokens of one sign, so that the formula itself gives infinities and few NaN."""
+    T, L, r, N, K = shape
+    rng = np.random.default_rng(T)
+    ids = rng.integers(-1, L, T)
+    ids[0] = 0
+    c = {"x": positive((T, K), 1), "A": positive((L, r, K), 2, 0.05), "B": positive((L, N, r), 3, 0.3),
+         "scale": torch.from_numpy(rng.uniform(0.5, 2, L).astype(np.float32)).to(DEV), "base": bf16((T, N), 4).to(DEV),
+         "dy": positive((T, N), 5, 2.0 ** -10), "dres": bf16((T, K), 6, 1e-3).to(DEV)}
+    t = c[where]
+    if where in ("x", "dy"):
+        some = np.nonzero(ids == 0)[0]
+        t[int(some[0]), 5] = value
+        t[int(some[-1]), t.shape[1] - 1] = value
+    else:
+        t[0, 3, 5] = value
+    got, want = check(lpq, c, ids, lpq.lpq_route_plan(torch.from_numpy(ids.astype(np.int32)).to(DEV), L))
+    if value == value and where != "dy":   # the infinities are there to be met
+        assert np.isinf(want[0]).any() and np.isinf(want[1 if where != "x" else 2]).any()
+
+
+@pytest.mark.parametrize("value", [float("inf"), -float("inf")])
+@pytest.mark.parametrize("shape", SHAPES)
+def test_infinities_beside_both_signs(lpq, shape, value):
+    """Infinite tokens and factors among numbers of both signs: each infinity goes by the sign that it meets, and
+    two that meet are a NaN."""
+    T, L, r, N, K = shape
+    ids = np.random.default_rng(T).integers(-1, L, T)
+    ids[:2] = 0
+    plan = lpq.lpq_route_plan(torch.from_numpy(ids.astype(np.int32)).to(DEV), L)
+    for where in ("x", "A", "B", "dy"):
+        c = {"x": bf16((T, K), 1).to(DEV), "A": bf16((L, r, K), 2, 0.05).to(DEV), "B": bf16((L, N, r), 3, 0.3).to(DEV),
+             "scale": torch.linspace(-1, 2, L, device=DEV), "base": bf16((T, N), 4).to(DEV), "dy": bf16((T, N), 5, 1e-3).to(DEV),
+             "dres": bf16((T, K), 6, 1e-3).to(DEV)}
+        c["scale"][0] = 0.75
+        c["A"][0][c["A"][0] == 0] = 0.5   # 0 times an infinity is another matter
+        c["B"][0][c["B"][0] == 0] = 0.5
+        if where in ("x", "dy"):
+            c[where][1, 3] = value
+        else:
+            c[where][0, 2, 1] = value
+        check(lpq, c, ids, plan)
+
+
+def test_above_the_largest_bf16(lpq):
+    """u and du between BF16's largest number and FP32's: finite, and their products as exact as others."""
+    high = 2.0 ** 63 * 1.9921875, 2.0 ** 62                    # of a token
+    low = 2.0 ** 64, 2.0 ** 57 * 1.0625                         # of the first factor
+    u = high[0] * low[0] + high[1] * low[1]                     # rounds to an infinity in BF16
+    assert 2.0 ** 127 * 1.9921875 < u < 2.0 ** 128 and np.float32(u) == u
+    for tokens, rank in ((3, 8), (200, 24), (200, 72)):
+        ids = np.arange(tokens) % 2
+        plan = plan_of(lpq, ids, 2)
+        N, K = 72, 40
+        x, first, second = np.zeros((tokens, K)), np.zeros((2, rank, K)), np.zeros((2, N, rank))
+        sign = np.where(np.arange(tokens) % 3 == 0, -1.0, 1.0)
+        x[:, :2] = sign[:, None] * np.array(high)
+        first[:, :, :2] = np.array(low)
+        for n in range(N):
+            second[:, n, n % rank] = (1 + n % 5) * 2.0 ** -121
+        want = torch.from_numpy(sign[:, None] * u * second.sum(2)[ids]).float().to(torch.bfloat16)   # one product: 13 bits by 3
+        assert bool(want.isfinite().all())
+        assert torch.equal(lpq.lpq_adapters(bf(x), bf(first), bf(second), *plan).cpu(), want)
+        dx, _, _ = lpq.lpq_adapters_backward(bf(x), bf(np.zeros((tokens, N))), bf(second.transpose(0, 2, 1)), bf(first.transpose(0, 2, 1)), *plan)
+        assert torch.equal(dx.cpu(), want)
+        # the FP32 gradients: one token of group 0 has the other factor, 2^-120
+        one = np.zeros((tokens, N))
+        one[0, 7] = 3 * 2.0 ** -121
+        _, _, dB = lpq.lpq_adapters_backward(bf(one), bf(x), bf(first), bf(np.zeros((2, N, rank))), *plan)
+        exact = np.zeros((2, N, rank))
+        exact[0, 7] = sign[0] * u * one[0, 7]
+        assert np.array_equal(f64(dB), exact)
+        _, dA, _ = lpq.lpq_adapters_backward(bf(x), bf(one), bf(np.zeros((2, rank, N))), bf(first.transpose(0, 2, 1)), *plan)
+        assert np.array_equal(f64(dA), exact.transpose(0, 2, 1))
