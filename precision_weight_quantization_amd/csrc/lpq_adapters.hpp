@@ -32,7 +32,7 @@ __device__ __forceinline__ v4f mfma_bf16(v4u a, v4u b, v4f c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, a), __builtin_bit_cast(v8bf, b), c, 0, 0, 0);
 }
 
-// The first 8 bits of each of 8 FP32 numbers as a BF16 vector; they keep what is left, which takes two more
+// The first 8 bits of each of N FP32 numbers as BF16 numbers; they keep what is left, which takes two more
 // of these.  FIRST: nothing is left of an infinity or a NaN (infinity - infinity would be a NaN).  Cut and not
 // rounded, so that no finite number becomes an infinity.
 template <bool FIRST, int N>
@@ -198,7 +198,8 @@ __device__ __forceinline__ ExpandRow<STEPS> expand_row(const ExpandArgs& A, cons
         float f[8];
         const int j = s * 32 + 8 * g;
         v4f a{}, b{};
-        if (e.in && j < A.rank) {
+        const bool there = e.in && j < A.rank;
+        if (there) {
             for (int i = 0; i < A.splits; i++) {
                 const v4f* p = reinterpret_cast<const v4f*>(A.u + ((int64_t)i * R.capacity + row) * A.rank + j);
                 a += load<false>(p);
@@ -206,7 +207,10 @@ __device__ __forceinline__ ExpandRow<STEPS> expand_row(const ExpandArgs& A, cons
             }
         }
 #pragma unroll
-        for (int i = 0; i < 4; i++) f[i] = a[i] * scale, f[4 + i] = b[i] * scale;
+        for (int i = 0; i < 4; i++) {   // past the rank zeros whatever the scale
+            f[i] = there ? a[i] * scale : 0.0f;
+            f[4 + i] = there ? b[i] * scale : 0.0f;
+        }
         e.hi[s] = take_bf16<true>(f);
         e.mid[s] = take_bf16<false>(f);
         e.lo[s] = take_bf16<false>(f);

@@ -142,7 +142,7 @@ def check(lpq, c, ids, plan):
 
 
 @pytest.mark.parametrize("value", [float("inf"), -float("inf"), float("nan")])
-@pytest.mark.parametrize("where", ["x", "dy", "A", "B"])
+@pytest.mark.parametrize("where", ["x", "dy", "A", "B", "scale"])
 @pytest.mark.parametrize("shape", SHAPES)
 def test_infinities_as_the_formula(lpq, shape, where, value):
     """Factors and tokens of one sign, so that the formula itself gives infinities and few NaN."""
@@ -158,6 +158,8 @@ def test_infinities_as_the_formula(lpq, shape, where, value):
         some = np.nonzero(ids == 0)[0]
         t[int(some[0]), 5] = value
         t[int(some[-1]), t.shape[1] - 1] = value
+    elif where == "scale":
+        t[0] = value
     else:
         t[0, 3, 5] = value
     got, want = check(lpq, c, ids, lpq.lpq_route_plan(torch.from_numpy(ids.astype(np.int32)).to(DEV), L))
