@@ -161,8 +161,10 @@ __global__ __launch_bounds__(64 * kShrinkWaves) void k_adapter_shrink(ShrinkPair
 #pragma unroll
         for (int i = 1; i < W; i++) s += part[i][y][lane];
         const int row = first + y % MT * 16 + r, j = y / MT * 16 + g * 4;   // 4 results: rank % 8 == 0
-        if (row < last && j < P.rank)
+        if (row < last && j < P.rank) {
+            if (!in_m[MT == 1 ? 0 : y % MT]) s = v4f{0.0f, 0.0f, 0.0f, 0.0f};   // padding, whatever the factor
             store<false>(reinterpret_cast<v4f*>(A.u + ((int64_t)split * R.capacity + row) * P.rank + j), s);
+        }
     }
 }
 

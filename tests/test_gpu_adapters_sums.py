@@ -190,6 +190,23 @@ def test_infinities_beside_both_signs(lpq, shape, value):
         check(lpq, c, ids, plan)
 
 
+@pytest.mark.parametrize("value", [float("inf"), float("nan")])
+@pytest.mark.parametrize("shape", SHAPES)
+def test_padding_beside_infinite_factors(lpq, shape, value):
+    """Padding rows of a group whose factors hold infinities or NaN add nothing to its gradients."""
+    T, L, r, N, K = shape
+    ids = np.random.default_rng(T).integers(0, L, T)
+    for where in ("A", "B"):
+        c = {"x": positive((T, K), 1), "A": positive((L, r, K), 2, 0.05), "B": positive((L, N, r), 3, 0.3),
+             "scale": torch.linspace(0.5, 2, L, device=DEV), "base": bf16((T, N), 4).to(DEV),
+             "dy": positive((T, N), 5, 2.0 ** -10), "dres": bf16((T, K), 6, 1e-3).to(DEV)}
+        c[where][0, 3, 5] = value
+        for align in (5, 64):
+            _, want = check(lpq, c, ids, plan_of(lpq, ids, L, align))
+            d = want[3 if where == "A" else 2][0]   # dB or dA of that adapter
+            assert value != value or np.isinf(d).any() and not np.isnan(d).any()
+
+
 def test_above_the_largest_bf16(lpq):
     """u and du between BF16's largest number and FP32's: finite, and their products as exact as others."""
     high = 2.0 ** 63 * 1.9921875, 2.0 ** 62                    # of a token
