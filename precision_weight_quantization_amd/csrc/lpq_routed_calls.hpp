@@ -206,9 +206,9 @@ struct Adapters {
     int32_t groups, rank;
     int64_t N, K;
 };
-// With these limits no launch below passes max_groups(), so that nothing is refused once a part is enqueued:
-// expand 2^22 workgroups of 256 threads (64 rows by 256 columns, 64 tokens to copy), gradient 2^22, transpose
-// 2^23, shrink 2^20 of 512.
+// The launches by rows or factors of these limits stay below max_groups(): shrinks 2^21 of 512 threads, gradients
+// 2^23 and planes 2^22 of 256.  Those by rows and columns together are counted by adapters_forward_shape() and
+// adapters_backward_shape(), so that nothing is refused once a part is enqueued.
 lpq_status adapters_shape(const Adapters& P) {
     const int64_t most = int64_t(1) << 35;
     if (P.groups <= 0 || P.groups > kRouteMaxGroups || P.rank <= 0 || P.rank > 128 || P.rank % 8) return LPQ_ERR_SHAPE;
@@ -257,24 +257,36 @@ lpq_status adapter_shrink(const Adapters& P, const Routing& R, const Factor& one
 
 // The expand's kernel: tiles of 64 rows where a group has as many on average; else 16 rows and 256
 // columns a wave, fewer columns where that leaves the card idle.
+struct ExpandShape {
+    bool tile;
+    int64_t columns;    // of a workgroup
+    int64_t copy_tiles, chunks, blocks;
+};
+ExpandShape expand_shape(const Adapters& P, int64_t n, int64_t copies) {
+    ExpandShape e{P.capacity / P.groups >= 64, kTileColumns, 0, 0, 0};
+    if (e.tile) {
+        e.copy_tiles = ceil_div(copies, 64 * kExpandWaves);
+        e.chunks = ceil_div(n, e.columns);
+        e.blocks = (e.copy_tiles + adapter_tiles(P, 4)) * e.chunks;
+        return e;
+    }
+    e.copy_tiles = ceil_div(copies, 64);
+    const int64_t rows = ceil_div(e.copy_tiles + adapter_tiles(P, 1), kExpandWaves);
+    e.columns = 256;
+    while (e.columns > 64 && rows * ceil_div(n, e.columns) < 4 * kComputeUnits) e.columns /= 2;
+    e.chunks = ceil_div(n, e.columns);
+    e.blocks = rows * e.chunks;
+    return e;
+}
 template <int STEPS>
 lpq_status adapter_expand(ExpandArgs A, const Adapters& P, const Routing& R, hipStream_t s) {
-    const int64_t copies = A.in == A.out ? 0 : P.tokens;
-    if (P.capacity / P.groups >= 64) {
-        A.copy_tiles = (int32_t)ceil_div(copies, 64 * kExpandWaves);
-        A.chunks = (int32_t)ceil_div(A.N, kTileColumns);
-        hipLaunchKernelGGL(k_adapter_expand_tile<STEPS>, dim3((unsigned)((A.copy_tiles + adapter_tiles(P, 4)) * A.chunks)), dim3(64 * kExpandWaves),
-                           0, s, A, R);
-        return launched();
-    }
-    A.copy_tiles = (int32_t)ceil_div(copies, 64);
-    const int64_t tiles = A.copy_tiles + adapter_tiles(P, 1);
-    int64_t columns = 256;
-    while (columns > 64 && ceil_div(tiles, kExpandWaves) * ceil_div(A.N, columns) < 4 * kComputeUnits) columns /= 2;
-    A.chunks = (int32_t)ceil_div(A.N, columns);
-    const dim3 grid((unsigned)(ceil_div(tiles, kExpandWaves) * A.chunks)), block(64 * kExpandWaves);
-    if (columns == 256) hipLaunchKernelGGL((k_adapter_expand<STEPS, 4>), grid, block, 0, s, A, R);
-    else if (columns == 128) hipLaunchKernelGGL((k_adapter_expand<STEPS, 2>), grid, block, 0, s, A, R);
+    const ExpandShape e = expand_shape(P, A.N, A.in == A.out ? 0 : P.tokens);
+    A.copy_tiles = (int32_t)e.copy_tiles;
+    A.chunks = (int32_t)e.chunks;
+    const dim3 grid((unsigned)e.blocks), block(64 * kExpandWaves);
+    if (e.tile) hipLaunchKernelGGL(k_adapter_expand_tile<STEPS>, grid, block, 0, s, A, R);
+    else if (e.columns == 256) hipLaunchKernelGGL((k_adapter_expand<STEPS, 4>), grid, block, 0, s, A, R);
+    else if (e.columns == 128) hipLaunchKernelGGL((k_adapter_expand<STEPS, 2>), grid, block, 0, s, A, R);
     else hipLaunchKernelGGL((k_adapter_expand<STEPS, 1>), grid, block, 0, s, A, R);
     return launched();
 }
@@ -337,14 +349,29 @@ lpq_status adapter_grad(const Adapters& P, const Routing& R, const Gradient (&g)
 }
 
 // A^T and B^T.
-lpq_status adapter_transpose(const Adapters& P, const uint16_t* A, uint16_t* At, const uint16_t* B, uint16_t* Bt, hipStream_t s) {
+AdapterTransposePair transpose_pair(const Adapters& P, const uint16_t* A, uint16_t* At, const uint16_t* B, uint16_t* Bt) {
     auto one = [&](const uint16_t* in, uint16_t* out, int64_t m, int64_t n) {
         const int32_t tm = (int32_t)ceil_div(m, 64), tn = (int32_t)ceil_div(n, 64);
         return AdapterTransposeArgs{in, out, (int32_t)m, (int32_t)n, tm, tn, P.groups * tm * tn};
     };
-    const AdapterTransposePair T{{one(A, At, P.rank, P.K), one(B, Bt, P.N, P.rank)}};
+    return {{one(A, At, P.rank, P.K), one(B, Bt, P.N, P.rank)}};
+}
+lpq_status adapter_transpose(const AdapterTransposePair& T, hipStream_t s) {
     hipLaunchKernelGGL(k_adapter_transpose, dim3((unsigned)(T.a[0].blocks + T.a[1].blocks)), dim3(256), 0, s, T);
     return launched();
+}
+
+lpq_status adapters_forward_shape(const Adapters& P) {
+    const lpq_status st = adapters_shape(P);
+    if (st != LPQ_OK) return st;
+    return expand_shape(P, P.N, P.tokens).blocks > max_groups(64 * kExpandWaves) ? LPQ_ERR_SHAPE : LPQ_OK;
+}
+lpq_status adapters_backward_shape(const Adapters& P) {
+    const lpq_status st = adapters_shape(P);
+    if (st != LPQ_OK) return st;
+    const AdapterTransposePair T = transpose_pair(P, nullptr, nullptr, nullptr, nullptr);
+    if ((int64_t)T.a[0].blocks + T.a[1].blocks > max_groups(256)) return LPQ_ERR_SHAPE;
+    return expand_shape(P, P.K, P.tokens).blocks > max_groups(64 * kExpandWaves) ? LPQ_ERR_SHAPE : LPQ_OK;
 }
 
 int64_t whole_lines(int64_t n) { return ceil_div(n, 256) * 256; }
@@ -355,14 +382,14 @@ extern "C" {
 
 int64_t lpq_adapters_workspace(int64_t tokens, int64_t capacity, int32_t groups, int32_t rank, int64_t N, int64_t K) {
     const Adapters P{tokens, capacity, groups, rank, N, K};
-    return adapters_shape(P) == LPQ_OK ? shrink_bytes(P, K) : 0;
+    return adapters_forward_shape(P) == LPQ_OK ? shrink_bytes(P, K) : 0;
 }
 
 lpq_status lpq_adapters(const uint16_t* x, const uint16_t* A, const uint16_t* B, const float* scale, const int32_t* offsets,
                         const int32_t* rows, const int32_t* src, int64_t tokens, int64_t capacity, int32_t groups, int32_t rank,
                         int64_t N, int64_t K, const uint16_t* base, uint16_t* y, void* workspace, int64_t workspace_bytes, void* stream) {
     const Adapters P{tokens, capacity, groups, rank, N, K};
-    lpq_status st = adapters_shape(P);
+    lpq_status st = adapters_forward_shape(P);
     if (st != LPQ_OK) return st;
     if (!x || !A || !B || !offsets || !rows || !src || !y || !workspace) return LPQ_ERR_NULL;
     if (!aligned(x, 16) || !aligned(A, 16) || !aligned(B, 16) || !aligned(base, 16) || !aligned(y, 16) || !aligned(workspace, 16) ||
@@ -384,7 +411,7 @@ lpq_status lpq_adapters(const uint16_t* x, const uint16_t* A, const uint16_t* B,
 
 int64_t lpq_adapters_backward_workspace(int64_t tokens, int64_t capacity, int32_t groups, int32_t rank, int64_t N, int64_t K) {
     const Adapters P{tokens, capacity, groups, rank, N, K};
-    if (adapters_shape(P) != LPQ_OK) return 0;
+    if (adapters_backward_shape(P) != LPQ_OK) return 0;
     const int64_t factor = 2 * (int64_t)groups * rank;
     return whole_lines(factor * K) + whole_lines(factor * N) + whole_lines(shrink_bytes(P, K)) + whole_lines(shrink_bytes(P, N)) +
            2 * whole_lines(planes_bytes(P)) + whole_lines(grad_bytes(P, K)) + grad_bytes(P, N);
@@ -395,7 +422,7 @@ lpq_status lpq_adapters_backward(const uint16_t* dy, const uint16_t* x, const ui
                                  int32_t groups, int32_t rank, int64_t N, int64_t K, const uint16_t* dres, uint16_t* dx, float* dA,
                                  float* dB, int accumulate, void* workspace, int64_t workspace_bytes, void* stream) {
     const Adapters P{tokens, capacity, groups, rank, N, K};
-    lpq_status st = adapters_shape(P);
+    lpq_status st = adapters_backward_shape(P);
     if (st != LPQ_OK) return st;
     if (!dy || !x || !A || !B || !offsets || !rows || !src || !dx || !dA || !dB || !workspace) return LPQ_ERR_NULL;
     if (!aligned(dy, 16) || !aligned(x, 16) || !aligned(A, 16) || !aligned(B, 16) || !aligned(dres, 16) || !aligned(dx, 16) ||
@@ -425,7 +452,7 @@ lpq_status lpq_adapters_backward(const uint16_t* dy, const uint16_t* x, const ui
     float* part_a = reinterpret_cast<float*>(take(grad_bytes(P, K)));
     float* part_b = reinterpret_cast<float*>(at);
     const int32_t parts = shrink_splits(P, K), dparts = shrink_splits(P, N);
-    if ((st = adapter_transpose(P, A, At, B, Bt, s)) != LPQ_OK) return st;
+    if ((st = adapter_transpose(transpose_pair(P, A, At, B, Bt), s)) != LPQ_OK) return st;
     if ((st = adapter_shrink(P, R, {x, A, u, K}, {dy, Bt, du, N}, src, s)) != LPQ_OK) return st;
     const AdapterPlanesArgs planes_args{{du, u}, {planes[0], planes[1]}, {dparts, parts}, rank, (int32_t)planes_pitch(P)};
     hipLaunchKernelGGL(k_adapter_planes, dim3((unsigned)(planes_pitch(P) / 64), (unsigned)ceil_div(rank, 16), 2), dim3(256), 0, s, planes_args, R);
