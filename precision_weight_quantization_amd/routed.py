@@ -8,6 +8,8 @@ data.  Indexes are ``torch.int32``.
 """
 from __future__ import annotations
 
+import math
+
 import torch
 
 import precision_weight_quantization_amd as _p
@@ -46,9 +48,15 @@ def lpq_route_capacity(pairs: int, groups: int, align: int = 1) -> int:
     return n
 
 
+def _part(t, shape):
+    """The first elements of a buffer that was passed in, in the shape of what the call wrote there."""
+    return t if t.shape == shape else t.view(-1)[:math.prod(shape)].view(shape)
+
+
 def lpq_route_plan(ids, groups, align=1, offsets=None, rows=None, src=None, workspace=None, stream=None):
     """The rows of each group: ids (int32 or int64, [tokens, k] or [tokens]; outside [0, groups): no row) ->
     (offsets [groups+1], rows like ids (-1: none), src [capacity], the pair of each row (-1: padding)), all int32.
+    offsets and rows passed in may be larger: what is returned is the part of them that holds the plan.
     A src passed in sets the capacity, at least ``lpq_route_capacity(ids.numel(), groups, align)`` rows."""
     _arg(ids, "ids", dtypes=(torch.int32, torch.int64))
     pairs = ids.numel()
@@ -71,7 +79,8 @@ def lpq_route_plan(ids, groups, align=1, offsets=None, rows=None, src=None, work
     _launch(_p._L.lpq_route_plan, "lpq_route_plan", ids, stream, ids.data_ptr(), ids.element_size(), pairs, groups, align,
             offsets.data_ptr(), rows.data_ptr(), src.data_ptr(), capacity, _ptr(workspace),
             0 if workspace is None else workspace.nbytes)
-    return offsets, rows, src
+    # of larger buffers the plan's part: the calls that read a plan take its sizes from these
+    return _part(offsets, (groups + 1,)), _part(rows, ids.shape), src
 
 
 def _tokens(rows, like, tokens=None):
