@@ -170,15 +170,20 @@ __device__ __forceinline__ int wave_offset(const Routing& R, int g) {
 }
 __device__ __forceinline__ RouteRun wave_run(const Routing& R, int g) { return route_run(R, wave_offset(R, g), wave_offset(R, g + 1)); }
 
-__device__ __forceinline__ int wave_scan(int v) {   // inclusive sums over the lanes
+// Inclusive sums over the lanes, of numbers from 0 to `most` (up to 2^30) and cut to it.
+__device__ __forceinline__ int wave_scan(int v, int most) {
     const int lane = threadIdx.x & 63;
 #pragma unroll
     for (int d = 1; d < 64; d *= 2) {
         const int up = __shfl_up(v, d);
-        if (lane >= d) v += up;
+        if (lane >= d) v = min(v + up, most);
     }
     return v;
 }
+
+// No plan has as many as kRouteMost: 2^30 rows are 2^26 tiles of 16, and a group's last tile another 2^10.  Groups
+// that overlap, which no plan has, would pass 32 bits and lead outside the buffers: so they are cut.
+constexpr int kRouteMost = 1 << 28;
 
 // Something that each group has a number of, end to end: tiles of its rows, or the cost of
 // its contraction.  A lane counts for its share of the groups once; the group of a place is
@@ -194,7 +199,7 @@ struct RouteMap {
         int mine = 0;
         for (int i = 0; i < share; i++)
             if (lane * share + i < R.groups) mine += count(lane_run(R, lane * share + i));
-        upto = wave_scan(mine);
+        upto = wave_scan(min(mine, kRouteMost), kRouteMost);
         total = __builtin_amdgcn_readlane(upto, 63);
     }
     // The group of place v < total, the same in every lane; its run, and the place within it.
