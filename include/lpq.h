@@ -651,9 +651,11 @@ lpq_status lpq_mx_matmul_routed_dw(const uint8_t* a, const uint8_t* ae, int a_fo
  * B: [groups, N, rank] BF16; scale: [groups] FP32, NULL: ones; base: [tokens, N] BF16, NULL:
  * zeros, and may be y itself; offsets, rows [tokens], src [capacity]: the plan's (any align).  K, N and
  * rank multiples of 8, rank up to 128, K and N up to 2^18, tokens and capacity up to 2^24, no
- * matrix above 2^35 elements, and no more rows by columns than one launch holds (capacity * N, in the backward
- * pass capacity * K, up to 2^35 always fit; LPQ_ERR_SHAPE before anything is enqueued); arrays 16-byte aligned, scale and the plan's 4.  Sums are FP32, and so is u = x A^T in between, in an order fixed by the
- * shape: a call's result does not vary.
+ * matrix above 2^35 elements, and no more rows by columns than one launch holds (capacity * N, in
+ * the backward pass capacity * K, up to 2^35 always fit; LPQ_ERR_SHAPE before anything is
+ * enqueued); arrays 16-byte aligned, scale and the plan's 4.  Sums are FP32, and so is u = x A^T in
+ * between, in an order fixed by the shape: a call's result does not vary.  Infinities and NaN show
+ * in the results that they are terms of.
  * Backward, from dy [tokens, N], with u and du = scale * dy B computed again:
  *   dx = BF16(dres + du A)    dres [tokens, K] BF16, NULL: zeros, and may be dx itself
  *   dA[g] (+)= sum over the tokens of g of du^T x          [groups, rank, K] FP32

@@ -14,14 +14,15 @@ namespace {
 //   expand    out[token] = in[token] + s_g U[row] W_g^T      contraction of `rank`
 //   gradient  V_g^T X_g over the rows of g        contraction over tokens
 //   transpose of A and B, for the backward pass's shrink and expand
-// Measured (us; floors at a copy's 5.2 TB/s): 8192 tokens of 8 adapters, 9728 x 2560, rank 64: shrink 24
-// (8: its time is 8 for finding rows and the sums in LDS, 7 for x and 9 for A out of the caches), expand 86 (62).  40
-// tokens of 32 adapters, 4096 x 2560, rank 16: 4.0 and 4.6, latency.  Gradients, 4099 tokens of 4, 1024 x 2560, rank
-// 24: transpose 4.8, shrinks 12.5, planes 4.8, gradients 20 and their sum 6.4, expand 14, together 60 (14): six
-// launches, each of a few round trips to memory.
+// Measured (us of device time, in a trace; floors at a copy's 5.2 TB/s): 8192 tokens of 8 adapters, 9728 x 2560, rank 64: shrink
+// 26 (8: its time is 8 for finding rows and the sums in LDS, 7 for x and 9 for A out of the caches), expand 90 (62: every XCD
+// reads every adapter's B).  40 tokens of 32 adapters, 4096 x 2560, rank 16: 4.2 and 5.5, latency.  Gradients, 4099 tokens of
+// 4, 1024 x 2560, rank 24: transpose 3.4, shrinks 13.6, planes 4.1, gradients 19.1 and their sum 6.1, expand 14.5, together 61
+// (14): transposes, planes and 12 MB of parts of 1.4 MB of gradients go through memory, in one or two steps of 32 rows a wave.
 // U is FP32.  It meets the BF16 matrix instruction as the sum of three BF16 numbers, which is all 24
 // bits.  Products of BF16 numbers are exact in FP32, so every sum is an FP32 one.  An infinity meets the
 // first of the three alone: the others may be zeros or of the other sign, which would make a NaN of it.
+// (Two numbers, 16 bits: 110 us a forward call of the first case; three 110; with the first's sums apart 112.)
 // Memory is the floor: x, base and y once, and the adapters' factors.
 typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
 
@@ -320,7 +321,7 @@ __global__ __launch_bounds__(64 * kExpandWaves) void k_adapter_expand(ExpandArgs
 // Many rows a group: a workgroup takes 64 rows, 16 a wave, and kTileColumns columns, 64 at a time.
 // Their weights (one piece of memory) go through LDS for all four waves, the next 64 columns' while
 // these are computed, with `in` two steps ahead.  (Each wave loading weights from the caches: 130 us
-// instead of 86 at 8192 x 9728, rank 64, of which 45 were those loads.)  A row of weights takes an odd number of
+// instead of 86 at 8192 x 9728, rank 64, of which 45 were those loads; both with u as two numbers.)  A row of weights takes an odd number of
 // 16-byte pieces in LDS, so that 16 rows' same piece lie in 16 different bank groups.
 constexpr int kTileColumns = 512;
 template <int STEPS>

@@ -147,8 +147,9 @@ struct RoutedLaunch {
 //  * Tiles by way of LDS from 6 rows on: 4 rows 69 in tiles of 64 rows and 73 by rows, but 27 and 25 with MXFP4
 //    weights (k = 768), 12 and 11 for 60 groups of 1024 x 1056; 6 rows 71 and 84; 8 rows 74 and 91. A tile's stages take
 //    as long as its weights, whatever its rows.
-//  * 128 x 64 tiles below 72 rows: 8 rows 74, with 128 x 128 81; 50 rows 108 and 107; 70 rows of 60 groups of 1024 x
-//    1056 20 and 24; 75 rows 120 and 112, evenly routed 139 and 101.
+//  * 128 x 64 tiles below 72 rows: 8 rows 74, with 128 x 128 81; 50 rows 108 and 107; 75 rows 120 and 112, evenly
+//    routed 139 and 101.  So the two are even from 50 rows on in MXFP8; the border is above 70 for products of two
+//    MXFP4 operands with few stages, 70 rows of 60 groups of 1024 x 1056 20 and 24.
 //  * 256 x 256 from 144 rows on (evenly routed): 75 rows 130 against 101 with 128 x 128, 125 rows 108 and 102 (MXFP4
 //    weights), 150 rows 123 and 149, 200 rows 134 and 157; 250 rows 186 and 178, where most groups just need a second
 //    tile.  256 x 128: 163 at 150 rows, 323 instead of 276 for the workload of 512.
@@ -157,6 +158,8 @@ struct RoutedLaunch {
 //    tokens 31, 27 and 25; where k is long the loads in flight count: 4 tokens, N = 4096, k = 7168 161 with 32, 186
 //    with 64).  Waves that share out k: of 3 steps at least (24 tokens, N = 2048, k = 768: 37 with 8, 31 with 2, 27 with
 //    1; 4 tokens, N = 4096, k = 7168: 167 with 8, 179 with 4).
+// The rule looks at capacity, which counts pairs without a row and padding too, and not at the number of tiles: 2
+// groups of 300 rows, N = 512, k = 2048 make 8 tiles of 256 x 256 and take 29 us, 5 of 190 rows, N = 930 20 tiles and 41.
 template <bool FP4A, bool FP4B>
 lpq_status mx_matmul_routed(const MatmulArgs& A, const Routing& R, hipStream_t s) {
     const RoutedLaunch<FP4A, FP4B, ROUTED_ROWS> L{A, R, s};
