@@ -15,9 +15,9 @@ namespace {
 //   gradient  V_g^T X_g over the rows of g        contraction over tokens
 //   transpose of A and B, for the backward pass's shrink and expand
 // Measured (us of device time, in a trace; floors at a copy's 5.2 TB/s): 8192 tokens of 8 adapters, 9728 x 2560, rank 64: shrink
-// 26 (8: its time is 8 for finding rows and the sums in LDS, 7 for x and 9 for A out of the caches), expand 90 (62: every XCD
+// 25 (8: its time is 8 for finding rows and the sums in LDS, 7 for x and 9 for A out of the caches), expand 88 (62: every XCD
 // reads every adapter's B).  40 tokens of 32 adapters, 4096 x 2560, rank 16: 4.2 and 5.5, latency.  Gradients, 4099 tokens of
-// 4, 1024 x 2560, rank 24: transpose 3.4, shrinks 13.6, planes 4.1, gradients 19.1 and their sum 6.1, expand 14.5, together 61
+// 4, 1024 x 2560, rank 24: transpose 3.3, shrinks 13.8, planes 4.0, gradients 19.5 and their sum 6.0, expand 14.6, together 61
 // (14): transposes, planes and 12 MB of parts of 1.4 MB of gradients go through memory, in one or two steps of 32 rows a wave.
 // U is FP32.  It meets the BF16 matrix instruction as the sum of three BF16 numbers, which is all 24
 // bits.  Products of BF16 numbers are exact in FP32, so every sum is an FP32 one.  An infinity meets the
