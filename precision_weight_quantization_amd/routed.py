@@ -41,7 +41,8 @@ def _outs(like, *specs):
 
 def lpq_route_capacity(pairs: int, groups: int, align: int = 1) -> int:
     """Rows that hold every routing of so many pairs, each group's rows padded to ``align``."""
-    n = _p._L.lpq_route_capacity(pairs, groups, align)
+    # the C call's 32-bit arguments would be the low bits of larger numbers
+    n = _p._L.lpq_route_capacity(pairs, groups, align) if 0 < pairs <= 1 << 30 and 0 < groups <= 1024 and 0 < align <= 1024 else 0
     if n == 0:
         raise ValueError(f"no plan of {pairs} pairs over {groups} groups with rows padded to {align}: 1 to 1024 groups, "
                          "1 to 1024 rows, up to 2^30 rows in all")

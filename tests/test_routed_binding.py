@@ -26,3 +26,14 @@ def test_the_plans_part_of_larger_buffers(runtime, monkeypatch, offsets, rows, i
         assert got[0] is o
     if rows == ids:
         assert got[1] is r
+
+
+@pytest.mark.parametrize("pairs,groups,align", [(8, (1 << 32) + 4, 1), (8, 4 - (1 << 32), 1), (8, 4, (1 << 32) + 1), (8, 4, 1 - (1 << 32)),
+                                                ((1 << 64) + 8, 4, 1), (8, 1 << 31, 1)])
+def test_sizes_beyond_their_c_types(pairs, groups, align):
+    """They are refused, not taken by their low bits."""
+    with pytest.raises(ValueError):
+        lpq.lpq_route_capacity(pairs, groups, align)
+    if pairs < 1 << 40:
+        with pytest.raises(ValueError):
+            lpq.lpq_route_plan(on1(I32, 4, 2), groups, align)
